@@ -698,6 +698,150 @@ bnn_status bnn_xnor_gemv_chain(const bnn_chain_layer* layers, int32_t L, const v
                                int32_t* y_i32, float* y_f32, uint32_t* acts, int64_t ld_acts, uint32_t* workspace,
                                bnn_stream_t stream);
 
+/* ------------------------------------------------------------------------
+ * 8-bit floating-point products with a scale per block of 128, and the
+ * routing of tokens to experts.  These serve the layers of a low-bit network
+ * that stay out of one bit ("Extreme Quantization ...": first and last layers
+ * kept at higher precision; the decode-shaped projections of the BitNet
+ * passage), for one token up to long prompts.  The pages give no formula for
+ * them; each is stated here.
+ *
+ * FP8 LAYOUT.  A matrix of codes is e4m3 bytes (sign, 4 exponent bits of bias
+ * 7, 3 mantissa bits; largest value 448; NaN 0x7F / 0xFF; no infinities),
+ * row r at byte r * ld with ld a multiple of 16 and >= bnn_fp8_ld_bytes(K) =
+ * K rounded up to a multiple of 16; bytes K .. bnn_fp8_ld_bytes(K) - 1 of a
+ * packed row are written as 0 and never used by a product.  Scales are fp32
+ * and block-major: the scale of row block i and K block b (elements 128 b ..
+ * 128 b + 127) is scales[b * ld_scales + i].  Row blocks are single rows
+ * (activations, 1 x 128) or 128 rows (weights, 128 x 128).  The value of an
+ * element is its code times its block's scale.
+ *
+ * A size of 0 is allowed where stated and launches nothing (pointers of empty
+ * arrays may then be NULL).
+ * ------------------------------------------------------------------------ */
+
+/* Bytes of one packed row of K codes (K rounded up to 16); -1 for K < 1. */
+int64_t bnn_fp8_ld_bytes(int64_t K);
+
+/* bnn_fp8_pack -- quantise a real matrix to e4m3 codes with block scales:
+ *   s = max(amax / 448, 2^-126), amax = the largest finite |x| of the block,
+ *   code = e4m3(x * (1 / s)), every step rounded to nearest even in fp32.
+ *   Infinities and NaN become the NaN code 0x7F (or 0xFF) and do not count for amax.
+ *   x        device, [x_rows, K] row-major, dtype dt, row stride ld_x >= K
+ *            elements.
+ *   row_index device int32 [rows] or NULL: packed row r is row row_index[r] of
+ *            x (the row_token of bnn_route gathers tokens by expert).  A
+ *            packed row whose index is outside [0, x_rows) is left as it was,
+ *            codes and scales.  NULL: row r, and rows <= x_rows.  Only with
+ *            block_rows 1.
+ *   block_rows 1 or 128.
+ *   codes    device [rows, ld_codes] bytes, 16-byte aligned (FP8 LAYOUT).
+ *   scales   device fp32 [ceil(K / 128), ld_scales], ld_scales >= the number of
+ *            row blocks, ceil(rows / block_rows).
+ *   rows may be 0.
+ *   Errors: INVALID_ARG, ALIGNMENT, UNSUPPORTED (row_index with block_rows
+ *   128; more than 2^31 - 1 thread blocks), CUDA. */
+bnn_status bnn_fp8_pack(const void* x, bnn_dtype dt, int64_t x_rows, int64_t K, int64_t ld_x,
+                        const int32_t* row_index, int64_t rows, int block_rows, uint8_t* codes, int64_t ld_codes,
+                        float* scales, int64_t ld_scales, bnn_stream_t stream);
+
+/* bnn_fp8_gemm -- the product of block-scaled e4m3 operands:
+ *   C[m, n] = sum_b sA[b, m] * sW[b, n / 128] * (sum_{k in block b} a[m, k] w[n, k])
+ * with fp32 sums (each block's on the tensor cores, the blocks' in registers)
+ * and one rounding to the output type.  M = 1 is the single-token form.
+ *   A        device [M, lda] codes, a_scales [ceil(K/128), ld_as] with a scale
+ *            per row (block_rows 1), ld_as >= M.
+ *   W        device [N, ldw] codes, w_scales [ceil(K/128), ld_ws] with a scale
+ *            per 128 rows (block_rows 128), ld_ws >= ceil(N / 128).
+ *   out      device fp32 or bf16 (out_dt) [M, ld_out], ld_out >= N.
+ *   A NaN code makes its row (column) of C NaN and nothing else.
+ *   M, N >= 0, K >= 1, each below 2^31 - 512.
+ *   Errors: INVALID_ARG, ALIGNMENT (A, W not 16-byte aligned, lda / ldw not a
+ *   multiple of 16), CUDA. */
+bnn_status bnn_fp8_gemm(const uint8_t* A, int64_t lda, const float* a_scales, int64_t ld_as, const uint8_t* W,
+                        int64_t ldw, const float* w_scales, int64_t ld_ws, int64_t M, int64_t N, int64_t K, void* out,
+                        bnn_dtype out_dt, int64_t ld_out, bnn_stream_t stream);
+
+/* bnn_fp8_gemm_grouped -- bnn_fp8_gemm for rows grouped by expert: rows
+ * offsets[e] .. offsets[e + 1] - 1 of A are multiplied by W[e].
+ *   A, a_scales, out  as bnn_fp8_gemm, with R rows.
+ *   offsets  device int32 [E + 1], not decreasing, within [0, R] (values
+ *            outside are taken as the nearest bound).  A group may be empty.
+ *            Rows before offsets[0] and from offsets[E] on are not computed
+ *            and their outputs are left as they were.
+ *   W        device, E matrices [N, ldw], w_stride bytes apart (a multiple of
+ *            16, >= N * ldw); w_scales: E matrices [ceil(K/128), ld_ws],
+ *            ws_stride >= 0 elements apart (one array [ceil(K/128), E * row
+ *            blocks], as one bnn_fp8_pack of all E * N rows writes it when
+ *            N % 128 == 0, has ld_ws = E * N / 128 and ws_stride = N / 128).
+ *   R, N, E >= 0, K >= 1; E <= 1024.
+ *   Errors: INVALID_ARG, ALIGNMENT, UNSUPPORTED (E > 1024), CUDA. */
+bnn_status bnn_fp8_gemm_grouped(const uint8_t* A, int64_t lda, const float* a_scales, int64_t ld_as, int64_t R,
+                                const int32_t* offsets, int64_t E, const uint8_t* W, int64_t ldw, int64_t w_stride,
+                                const float* w_scales, int64_t ld_ws, int64_t ws_stride, int64_t N, int64_t K,
+                                void* out, bnn_dtype out_dt, int64_t ld_out, bnn_stream_t stream);
+
+/* Scores of bnn_route. */
+typedef enum bnn_route_score {
+    BNN_ROUTE_SOFTMAX = 0,       /* softmax over the experts */
+    BNN_ROUTE_SIGMOID = 1        /* 1 / (1 + exp(-logit)), each expert by itself */
+} bnn_route_score;
+
+/* How bnn_route chooses (host struct). */
+typedef struct bnn_route_params {
+    int32_t score;               /* one bnn_route_score value */
+    int32_t k;                   /* experts per token, 1 .. 16, <= E */
+    int32_t n_groups;            /* groups of E / n_groups consecutive experts, 1 .. 32; 1: no groups */
+    int32_t kept_groups;         /* groups a token may choose from, 1 .. n_groups */
+    int32_t group_top;           /* a group's score: 1 its largest choice value, 2 the sum of its two largest */
+    int32_t renormalize;         /* 1: the k weights are divided by their sum */
+    double scale;                /* factor on every weight (finite) */
+    const float* bias;           /* device fp32 [E] or NULL: added to the scores for the choice, not to the weights */
+} bnn_route_params;
+
+/* bnn_route -- choose k experts for each token from its router logits, and
+ * plan the experts' rows:
+ *   score_e  softmax or sigmoid of the logits;  choice_e = score_e + bias_e;
+ *   the kept_groups groups with the largest group score stay; of their
+ *   experts the k with the largest choice are taken, in that order;
+ *   weight_j = score of the j-th, divided by the sum of the k if renormalize,
+ *   times scale.
+ * Scores and comparisons are in fp64 (a choice is a whole number: fp32 ties
+ * would make it depend on rounding); equal values go to the lowest index.  An
+ * expert whose logit is NaN or -inf, or whose bias is NaN or -inf, is never
+ * chosen; a logit of +inf counts as the largest finite fp32.  A token with
+ * fewer than k experts to choose from gets index -1 and weight 0 in its last
+ * slots.
+ *   logits   device [T, ld], ld >= E, dtype dt; E 1 .. 512.
+ *   idx      device int32 [T, k], contiguous; weights device fp32 [T, k].
+ *   offsets, row_token, slot_row  device int32, all three or none (NULL): the
+ *            slots (t, j) sorted by expert, each expert's in the order of
+ *            t * k + j:
+ *            offsets[e] the first row of expert e, offsets[E] the rows in use
+ *            ([E + 1]); row_token[r] the token of row r, -1 from offsets[E] on
+ *            ([T * k]); slot_row[t * k + j] the row of the slot, -1 where idx
+ *            is -1 ([T * k]).
+ *   T >= 0, T * k < 2^31 - 1024.  With T = 0 and a plan, offsets are written as 0.
+ *   The results do not depend on the launch: no atomic orders them.
+ *   Errors: INVALID_ARG, ALIGNMENT, UNSUPPORTED (E > 512, k > 16), CUDA. */
+bnn_status bnn_route(const void* logits, bnn_dtype dt, int64_t T, int64_t E, int64_t ld,
+                     const bnn_route_params* params, int32_t* idx, float* weights, int32_t* offsets,
+                     int32_t* row_token, int32_t* slot_row, bnn_stream_t stream);
+
+/* bnn_route_combine -- the experts' rows back to their tokens:
+ *   out[t, n] = sum_j weights[t, j] * Y[slot_row[t, j], n],
+ * in fp32, by fused multiply-adds in j order, with one rounding to the output
+ * type.  A slot whose row is outside [0, R) is left out of the sum (its
+ * weight and no row are read).
+ *   Y        device [R, ld_y], dtype dt; slot_row int32 and weights fp32
+ *            [T, k], contiguous; out device [T, ld_out], dtype out_dt, not
+ *            overlapping Y.  k >= 1, T, N, R >= 0.
+ *   Errors: INVALID_ARG, ALIGNMENT (pointers not aligned to their element),
+ *   UNSUPPORTED (k > 64), CUDA. */
+bnn_status bnn_route_combine(const void* Y, bnn_dtype dt, int64_t R, int64_t N, int64_t ld_y, const int32_t* slot_row,
+                             const float* weights, int64_t T, int64_t k, void* out, bnn_dtype out_dt, int64_t ld_out,
+                             bnn_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

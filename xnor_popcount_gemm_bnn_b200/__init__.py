@@ -43,6 +43,9 @@ BNN_GEMM_ENGINE_POPCOUNT = 1
 BNN_GEMM_ENGINE_TENSOR = 2
 BNN_GEMM_ENGINE_TENSOR_I8 = 3
 
+BNN_ROUTE_SOFTMAX = 0
+BNN_ROUTE_SIGMOID = 1
+
 # Every symbol declared in include/bnn.h.
 EXPORTS = (
     "bnn_packed_ld_words", "bnn_conv3x3_ld_words", "bnn_status_string", "bnn_device_error",
@@ -53,7 +56,8 @@ EXPORTS = (
     "bnn_ternary_gemv_i8", "bnn_ternary_pack_noalloc", "bnn_pack_sign_rsign", "bnn_pack_sign_nchw_rsign",
     "bnn_binary_conv1x1_fused", "bnn_probe_int_pipes", "bnn_pack_bit_planes", "bnn_bitserial_gemm",
     "bnn_binary_bases_gemm", "bnn_binary_weight_gemv_i8", "bnn_gemv_chain_workspace_words",
-    "bnn_xnor_gemv_chain",
+    "bnn_xnor_gemv_chain", "bnn_fp8_ld_bytes", "bnn_fp8_pack", "bnn_fp8_gemm", "bnn_fp8_gemm_grouped", "bnn_route",
+    "bnn_route_combine",
 )
 
 
@@ -72,6 +76,12 @@ class bnn_epilogue(ctypes.Structure):
 class bnn_chain_layer(ctypes.Structure):
     _fields_ = [("W", ctypes.c_void_p), ("ldw", ctypes.c_int64), ("N", ctypes.c_int64),
                 ("popc_thresh", ctypes.c_void_p), ("thresh_mode", ctypes.c_void_p), ("alpha", ctypes.c_void_p)]
+
+
+class bnn_route_params(ctypes.Structure):
+    _fields_ = [("score", ctypes.c_int32), ("k", ctypes.c_int32), ("n_groups", ctypes.c_int32),
+                ("kept_groups", ctypes.c_int32), ("group_top", ctypes.c_int32), ("renormalize", ctypes.c_int32),
+                ("scale", ctypes.c_double), ("bias", ctypes.c_void_p)]
 
 
 def _load() -> ctypes.CDLL:
@@ -117,6 +127,13 @@ def _load() -> ctypes.CDLL:
         "bnn_binary_weight_gemv_i8": (i32, [p, i64, p, i64, i64, p, i32, p, p, p, ctypes.c_uint32, p]),
         "bnn_gemv_chain_workspace_words": (i64, []),
         "bnn_xnor_gemv_chain": (i32, [ctypes.POINTER(bnn_chain_layer), i32, p, i32, i64, p, p, p, i64, p, p]),
+        "bnn_fp8_ld_bytes": (i64, [i64]),
+        "bnn_fp8_pack": (i32, [p, i32, i64, i64, i64, p, i64, i32, p, i64, p, i64, p]),
+        "bnn_fp8_gemm": (i32, [p, i64, p, i64, p, i64, p, i64, i64, i64, i64, p, i32, i64, p]),
+        "bnn_fp8_gemm_grouped": (i32, [p, i64, p, i64, i64, p, i64, p, i64, i64, p, i64, i64, i64, i64, p, i32, i64,
+                                       p]),
+        "bnn_route": (i32, [p, i32, i64, i64, i64, ctypes.POINTER(bnn_route_params), p, p, p, p, p, p]),
+        "bnn_route_combine": (i32, [p, i32, i64, i64, i64, p, p, i64, i64, p, i32, i64, p]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -533,6 +550,142 @@ def bnn_binary_bases_gemm(H: torch.Tensor, J: int, B: torch.Tensor, I: int, K: i
     _check("bnn_binary_bases_gemm", _lib.bnn_binary_bases_gemm(
         _ptr(H), _ld(H), int(J), _ptr(B), _ld(B), int(I), M, N, int(K), _ptr(beta), _ptr(alpha), _ld(alpha),
         _ptr(Y), _ld(Y), _stream(stream)))
+
+
+# --------------------------------------------------------------------------
+# 8-bit block-scaled products and the routing to experts
+# --------------------------------------------------------------------------
+
+_CODES = (torch.float8_e4m3fn, torch.uint8)
+
+
+def _same_device(*tensors: Optional[torch.Tensor]) -> None:
+    """Kernels launch on the current CUDA device: every tensor has to be there."""
+    d = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and (not t.is_cuda or t.get_device() != d):
+            raise ValueError(f"a tensor on {t.device}, with cuda:{d} as the current device")
+
+
+def bnn_fp8_ld_bytes(K: int) -> int:
+    return int(_lib.bnn_fp8_ld_bytes(int(K)))
+
+
+def bnn_fp8_pack(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, block_rows: int = 1,
+                 row_index: Optional[torch.Tensor] = None, K: Optional[int] = None, stream=None) -> None:
+    """x [x_rows, K] (fp32/bf16, unit inner stride) -> e4m3 codes [rows, ld] (float8_e4m3fn or uint8) and block-major
+    fp32 scales [ceil(K / 128), row blocks].  row_index int32 [rows]: the row of x of each packed row (block_rows 1)."""
+    _same_device(x, codes, scales, row_index)
+    x_rows, Kx = x.shape
+    rows = codes.shape[0]
+    K = Kx if K is None else int(K)
+    if x.stride(1) != 1 or codes.stride(1) != 1 or scales.stride(1) != 1 or codes.dtype not in _CODES or \
+            scales.dtype != torch.float32 or K > Kx or scales.shape[0] < (K + 127) // 128 or \
+            codes.shape[1] < bnn_fp8_ld_bytes(K) or scales.shape[1] < -(-rows // int(block_rows)):
+        raise ValueError("codes [rows, ld >= K rounded up to 16] and fp32 scales [blocks of K, row blocks], unit inner stride")
+    if row_index is not None and (row_index.dtype != torch.int32 or tuple(row_index.shape) != (rows,) or
+                                  row_index.stride(0) != 1):
+        raise ValueError("row_index is a contiguous int32 [rows]")
+    _check("bnn_fp8_pack", _lib.bnn_fp8_pack(
+        _ptr(x), _dtype(x), x_rows, K, _row_stride(x), _ptr(row_index), rows, int(block_rows), _ptr(codes),
+        _row_stride(codes), _ptr(scales), _row_stride(scales), _stream(stream)))
+
+
+def _row_stride(t: torch.Tensor) -> int:
+    """Row stride of a matrix, at least its width (torch leaves the stride of a single row arbitrary)."""
+    return t.stride(-2) if t.shape[-2] > 1 else max(t.stride(-2), t.shape[-1])
+
+
+def bnn_fp8_gemm(A: torch.Tensor, a_scales: torch.Tensor, W: torch.Tensor, w_scales: torch.Tensor, K: int,
+                 out: torch.Tensor, stream=None) -> None:
+    """out [M, N] (fp32/bf16) = A W^T for codes A [M, lda], W [N, ldw] with scales [ceil(K / 128), M] (one per row)
+    and [ceil(K / 128), ceil(N / 128)] (one per 128 rows)."""
+    M, N, K = A.shape[0], W.shape[0], int(K)
+    _same_device(A, a_scales, W, w_scales, out)
+    _check_fp8(A, a_scales, W, w_scales, M, N, K, out)
+    _check("bnn_fp8_gemm", _lib.bnn_fp8_gemm(
+        _ptr(A), _row_stride(A), _ptr(a_scales), _row_stride(a_scales), _ptr(W), _row_stride(W), _ptr(w_scales),
+        _row_stride(w_scales), M, N, K, _ptr(out), _dtype(out), _row_stride(out), _stream(stream)))
+
+
+def bnn_fp8_gemm_grouped(A: torch.Tensor, a_scales: torch.Tensor, offsets: torch.Tensor, W: torch.Tensor,
+                         w_scales: torch.Tensor, K: int, out: torch.Tensor, stream=None) -> None:
+    """Rows offsets[e] .. offsets[e + 1] of A [R, lda] times W[e]^T for W [E, N, ldw], w_scales
+    [E, ceil(K / 128), ceil(N / 128)], offsets int32 [E + 1] on the device; out [R, N]."""
+    R, K = A.shape[0], int(K)
+    E, N = W.shape[:2]
+    _same_device(A, a_scales, offsets, W, w_scales, out)
+    if offsets.dtype != torch.int32 or tuple(offsets.shape) != (E + 1,) or offsets.stride(0) != 1 or \
+            W.dim() != 3 or w_scales.dim() != 3 or w_scales.shape[0] != E:
+        raise ValueError("offsets int32 [E + 1], W [E, N, ld], w_scales [E, blocks of K, row blocks]")
+    _check_fp8(A, a_scales, W, w_scales, R, N, K, out)
+    _check("bnn_fp8_gemm_grouped", _lib.bnn_fp8_gemm_grouped(
+        _ptr(A), _row_stride(A), _ptr(a_scales), _row_stride(a_scales), R, _ptr(offsets), E, _ptr(W), _row_stride(W),
+        W.stride(0) if E > 1 else N * _row_stride(W), _ptr(w_scales), _row_stride(w_scales), w_scales.stride(0), N, K,
+        _ptr(out), _dtype(out), _row_stride(out), _stream(stream)))
+
+
+def _check_fp8(A, a_scales, W, w_scales, M, N, K, out) -> None:
+    kb, ld = (K + 127) // 128, (K + 15) // 16 * 16
+    if A.dtype not in _CODES or W.dtype not in _CODES or a_scales.dtype != torch.float32 or \
+            w_scales.dtype != torch.float32:
+        raise ValueError("codes are float8_e4m3fn or uint8, scales float32")
+    if A.shape[1] < ld or W.shape[-1] < ld or a_scales.shape[0] < kb or a_scales.shape[1] < M or \
+            w_scales.shape[-2] < kb or w_scales.shape[-1] < (N + 127) // 128 or tuple(out.shape) != (M, N):
+        raise ValueError("sizes of codes, scales and out do not fit M, N and K")
+    if A.stride(-1) != 1 or W.stride(-1) != 1 or a_scales.stride(-1) != 1 or w_scales.stride(-1) != 1 or \
+            (out.stride(-1) != 1 and N > 1):
+        raise ValueError("unit inner strides")
+
+
+def bnn_route(logits: torch.Tensor, idx: torch.Tensor, weights: torch.Tensor, score: int = BNN_ROUTE_SOFTMAX,
+              bias: Optional[torch.Tensor] = None, n_groups: int = 1, kept_groups: int = 1, group_top: int = 2,
+              renormalize: bool = True, scale: float = 1.0, offsets: Optional[torch.Tensor] = None,
+              row_token: Optional[torch.Tensor] = None, slot_row: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Choose k experts per token: logits [T, E] (fp32/bf16) -> idx int32 [T, k], weights fp32 [T, k]; with offsets
+    int32 [E + 1], row_token int32 [T * k] and slot_row int32 [T, k] also the plan of rows by expert."""
+    T, E = logits.shape
+    k = idx.shape[1]
+    _same_device(logits, idx, weights, bias, offsets, row_token, slot_row)
+    if idx.dtype != torch.int32 or weights.dtype != torch.float32 or tuple(idx.shape) != (T, k) or \
+            tuple(weights.shape) != (T, k) or not idx.is_contiguous() or not weights.is_contiguous() or \
+            (logits.stride(1) != 1 and E > 1):
+        raise ValueError("logits [T, E] of unit inner stride, idx int32 [T, k] and weights float32 [T, k], contiguous")
+    for t, n in ((offsets, E + 1), (row_token, T * k), (slot_row, T * k)):
+        if t is not None and (t.dtype != torch.int32 or t.numel() != n or not t.is_contiguous()):
+            raise ValueError("offsets int32 [E + 1], row_token int32 [T * k], slot_row int32 [T, k], contiguous")
+    if bias is not None and (bias.dtype != torch.float32 or tuple(bias.shape) != (E,) or not bias.is_contiguous()):
+        raise ValueError("bias is a contiguous float32 [E]")
+    p = bnn_route_params(int(score), k, int(n_groups), int(kept_groups), int(group_top), int(bool(renormalize)),
+                         float(scale), _ptr(bias))
+    _check("bnn_route", _lib.bnn_route(
+        _ptr(logits), _dtype(logits), T, E, _row_stride(logits), ctypes.byref(p), _ptr(idx), _ptr(weights),
+        _ptr(offsets), _ptr(row_token), _ptr(slot_row), _stream(stream)))
+
+
+def bnn_route_combine(Y: torch.Tensor, slot_row: torch.Tensor, weights: torch.Tensor, out: torch.Tensor,
+                      stream=None) -> None:
+    """out [T, N] = sum over j of weights[t, j] * Y[slot_row[t, j]] (Y [R, N], fp32/bf16)."""
+    T, k = weights.shape
+    R, N = Y.shape
+    _same_device(Y, slot_row, weights, out)
+    if slot_row.dtype != torch.int32 or weights.dtype != torch.float32 or slot_row.numel() != T * k or \
+            not slot_row.is_contiguous() or not weights.is_contiguous() or tuple(out.shape) != (T, N) or \
+            (N > 1 and (Y.stride(1) != 1 or out.stride(1) != 1)):
+        raise ValueError("slot_row int32 [T, k] and weights float32 [T, k], contiguous; Y [R, N], out [T, N]")
+    _check("bnn_route_combine", _lib.bnn_route_combine(
+        _ptr(Y), _dtype(Y), R, N, _row_stride(Y), _ptr(slot_row), _ptr(weights), T, k, _ptr(out), _dtype(out),
+        _row_stride(out), _stream(stream)))
+
+
+def empty_fp8(rows: int, K: int, device="cuda") -> torch.Tensor:
+    """Storage for e4m3 codes [rows, bnn_fp8_ld_bytes(K)]."""
+    return torch.empty(rows, bnn_fp8_ld_bytes(K), dtype=torch.float8_e4m3fn, device=device)
+
+
+def empty_fp8_scales(rows: int, K: int, block_rows: int = 1, device="cuda") -> torch.Tensor:
+    """Storage for block-major scales [ceil(K / 128), ceil(rows / block_rows)]."""
+    return torch.empty((K + 127) // 128, -(-rows // block_rows), dtype=torch.float32, device=device)
 
 
 def empty_packed(rows: int, K: int, device="cuda") -> torch.Tensor:

@@ -2,7 +2,7 @@
 // arguments, encodes TMA descriptors, picks launch shapes and launches on the
 // caller's stream; every step of the computation runs in the kernels of
 // pack.cuh, gemm_popc.cuh, gemm_tc.cuh, gemm_f4.cuh, gemv.cuh, chain.cuh, bwgemv.cuh, conv.cuh,
-// conv_tc.cuh and ternary.cuh.
+// conv_tc.cuh, ternary.cuh, fp8.cuh, fp8_gemm.cuh and route.cuh.
 #include <cudaTypedefs.h>
 
 #include <atomic>
@@ -26,8 +26,11 @@
 #include "hostio.cuh"
 #include "bwgemv.cuh"
 #include "bwgemv_i8.cuh"
+#include "fp8.cuh"
+#include "fp8_gemm.cuh"
 #include "pack.cuh"
 #include "probe.cuh"
+#include "route.cuh"
 #include "ternary.cuh"
 
 namespace {
@@ -1695,6 +1698,225 @@ bnn_status bnn_xnor_gemv_chain(const bnn_chain_layer* layers, int32_t L, const v
         (void)cudaGetLastError();
         return BNN_ERR_CUDA;
     }
+    return launch_status();
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------------------
+// 8-bit block-scaled products and the routing to experts
+// ---------------------------------------------------------------------------
+namespace {
+
+inline bool real_dtype(int dt) { return dt == BNN_F32 || dt == BNN_BF16; }
+inline int64_t dtype_bytes(int dt) { return dt == BNN_F32 ? 4 : 2; }
+constexpr int64_t kMaxDim = INT_MAX - 512;       // tile arithmetic stays within int
+
+// Arguments that the dense and the grouped product share.
+bnn_status check_fp8_product(const uint8_t* A, int64_t lda, const float* sa, int64_t ldsa, const uint8_t* W,
+                             int64_t ldw, const float* sw, int64_t ldsw, int64_t M, int64_t N, int64_t K,
+                             const void* out, int out_dt, int64_t ldo) {
+    if (!real_dtype(out_dt) || M < 0 || N < 0 || K < 1 || M > kMaxDim || N > kMaxDim || K > kMaxDim)
+        return BNN_ERR_INVALID_ARG;
+    const bool empty = M == 0 || N == 0;                  // nothing is read or written: no pointer is needed
+    if (!empty && (A == nullptr || sa == nullptr || W == nullptr || sw == nullptr || out == nullptr))
+        return BNN_ERR_INVALID_ARG;
+    const int64_t ld = bnn_fp8_ld_bytes(K);
+    if (lda < ld || ldw < ld || ldsa < M || ldsw < ceil_div(N, bnn::fp8::BLOCK) || ldo < N)
+        return BNN_ERR_INVALID_ARG;
+    if (lda % 16 != 0 || ldw % 16 != 0 || !aligned(A, 16) || !aligned(W, 16)) return BNN_ERR_ALIGNMENT;
+    if (!aligned(sa, 4) || !aligned(sw, 4) || !aligned(out, (uintptr_t)dtype_bytes(out_dt))) return BNN_ERR_ALIGNMENT;
+    return BNN_OK;
+}
+
+bnn_status launch_fp8_gemm(const bnn::Fp8Gemm& g, int out_dt, cudaStream_t stream) {
+    const dim3 grid((unsigned)ceil_div(g.N, 64), (unsigned)ceil_div(g.R, 64), (unsigned)g.E);
+    if (out_dt == BNN_F32) bnn::fp8_gemm_simple_kernel<float><<<grid, 256, 0, stream>>>(g);
+    else bnn::fp8_gemm_simple_kernel<__nv_bfloat16><<<grid, 256, 0, stream>>>(g);
+    return launch_status();
+}
+
+template <typename T, int ALIGN>
+void launch_fp8_pack(const void* x, int64_t x_rows, int64_t K, int64_t ld_x, const int32_t* row_index, int64_t rows,
+                     int block_rows, uint8_t* codes, int64_t ldc, float* scales, int64_t lds, unsigned grid,
+                     int64_t tasks, cudaStream_t stream) {
+    const T* xt = static_cast<const T*>(x);
+    if (block_rows == 1)
+        bnn::fp8_pack_rows_kernel<T, ALIGN, 2><<<grid, 256, 0, stream>>>(xt, x_rows, K, ld_x, row_index, rows, codes,
+                                                                         ldc, scales, lds, tasks);
+    else
+        bnn::fp8_pack_blocks_kernel<T, ALIGN><<<grid, 256, 0, stream>>>(xt, rows, K, ld_x, codes, ldc, scales, lds,
+                                                                        ceil_div(K, bnn::fp8::BLOCK));
+}
+
+template <typename T>
+void launch_route_topk(const void* logits, const bnn::RouteParams& p, cudaStream_t stream) {
+    const T* l = static_cast<const T*>(logits);
+    const unsigned grid = (unsigned)ceil_div(p.T, 8);
+    if (p.E <= 64) bnn::route_topk_kernel<T, 2><<<grid, 256, 0, stream>>>(l, p);
+    else if (p.E <= 128) bnn::route_topk_kernel<T, 4><<<grid, 256, 0, stream>>>(l, p);
+    else if (p.E <= 256) bnn::route_topk_kernel<T, 8><<<grid, 256, 0, stream>>>(l, p);
+    else bnn::route_topk_kernel<T, 16><<<grid, 256, 0, stream>>>(l, p);
+}
+
+template <typename T, typename O>
+void launch_route_combine(const void* Y, int64_t R, int64_t N, int64_t ldy, const int32_t* slot_row,
+                          const float* weights, int64_t T_, int64_t k, void* out, int64_t ldo, cudaStream_t stream) {
+    const dim3 grid((unsigned)T_, (unsigned)ceil_div(N, 256));
+    bnn::route_combine_kernel<T, O><<<grid, 256, 0, stream>>>(static_cast<const T*>(Y), R, N, ldy, slot_row, weights,
+                                                             (int)k, static_cast<O*>(out), ldo);
+}
+
+}  // namespace
+
+extern "C" {
+
+int64_t bnn_fp8_ld_bytes(int64_t K) { return K < 1 ? -1 : (K + 15) / 16 * 16; }
+
+bnn_status bnn_fp8_pack(const void* x, bnn_dtype dt, int64_t x_rows, int64_t K, int64_t ld_x,
+                        const int32_t* row_index, int64_t rows, int block_rows, uint8_t* codes, int64_t ld_codes,
+                        float* scales, int64_t ld_scales, bnn_stream_t stream) {
+    using namespace bnn::fp8;
+    if (!real_dtype(dt)) return BNN_ERR_INVALID_ARG;
+    if (rows > 0 && ((x == nullptr && x_rows > 0) || codes == nullptr || scales == nullptr)) return BNN_ERR_INVALID_ARG;
+    if (x_rows < 0 || rows < 0 || K < 1 || ld_x < K || (block_rows != 1 && block_rows != BLOCK))
+        return BNN_ERR_INVALID_ARG;
+    if (x_rows > kMaxDim || rows > kMaxDim || K > kMaxDim) return BNN_ERR_INVALID_ARG;
+    if (row_index == nullptr && rows > x_rows) return BNN_ERR_INVALID_ARG;
+    if (ld_codes < bnn_fp8_ld_bytes(K) || ld_scales < ceil_div(rows, block_rows)) return BNN_ERR_INVALID_ARG;
+    if (ld_codes % 16 != 0 || !aligned(codes, 16) || !aligned(scales, 4) ||
+        !aligned(x, (uintptr_t)dtype_bytes(dt)) || (row_index != nullptr && !aligned(row_index, 4)))
+        return BNN_ERR_ALIGNMENT;
+    if (row_index != nullptr && block_rows != 1) return BNN_ERR_UNSUPPORTED;
+    if (rows == 0) return BNN_OK;
+    const int64_t es = dtype_bytes(dt);
+    // Rows kernel: a warp takes two 16-byte vectors per lane of one row.
+    const int64_t tasks = rows * ceil_div(K, 2 * 32 * (16 / es));
+    const int64_t grid = block_rows == 1 ? ceil_div(tasks, 8) : ceil_div(rows, BLOCK) * ceil_div(K, BLOCK);
+    if (grid > INT_MAX) return BNN_ERR_UNSUPPORTED;
+    const int64_t row_bytes = ld_x * es;
+    const int a = aligned(x, 16) && row_bytes % 16 == 0 ? 16 : aligned(x, 8) && row_bytes % 8 == 0 ? 8 : 4;
+    cudaStream_t s = as_cuda(stream);
+#define BNN_PACK(T, A) \
+    launch_fp8_pack<T, A>(x, x_rows, K, ld_x, row_index, rows, block_rows, codes, ld_codes, scales, ld_scales, \
+                          (unsigned)grid, tasks, s)
+    if (dt == BNN_F32) {
+        if (a == 16) BNN_PACK(float, 16);
+        else if (a == 8) BNN_PACK(float, 8);
+        else BNN_PACK(float, 4);
+    } else {
+        if (a == 16) BNN_PACK(__nv_bfloat16, 16);
+        else if (a == 8) BNN_PACK(__nv_bfloat16, 8);
+        else BNN_PACK(__nv_bfloat16, 4);
+    }
+#undef BNN_PACK
+    return launch_status();
+}
+
+bnn_status bnn_fp8_gemm(const uint8_t* A, int64_t lda, const float* a_scales, int64_t ld_as, const uint8_t* W,
+                        int64_t ldw, const float* w_scales, int64_t ld_ws, int64_t M, int64_t N, int64_t K, void* out,
+                        bnn_dtype out_dt, int64_t ld_out, bnn_stream_t stream) {
+    const bnn_status st =
+        check_fp8_product(A, lda, a_scales, ld_as, W, ldw, w_scales, ld_ws, M, N, K, out, out_dt, ld_out);
+    if (st != BNN_OK) return st;
+    if (M == 0 || N == 0) return BNN_OK;
+    const bnn::Fp8Gemm g{A,  lda,  a_scales, ld_as, W,   ldw,     0,       w_scales, ld_ws,
+                         0,  nullptr, (int)M, 1,    (int)N, (int)K, out, ld_out};
+    return launch_fp8_gemm(g, out_dt, as_cuda(stream));
+}
+
+bnn_status bnn_fp8_gemm_grouped(const uint8_t* A, int64_t lda, const float* a_scales, int64_t ld_as, int64_t R,
+                                const int32_t* offsets, int64_t E, const uint8_t* W, int64_t ldw, int64_t w_stride,
+                                const float* w_scales, int64_t ld_ws, int64_t ws_stride, int64_t N, int64_t K,
+                                void* out, bnn_dtype out_dt, int64_t ld_out, bnn_stream_t stream) {
+    const bnn_status st =
+        check_fp8_product(A, lda, a_scales, ld_as, W, ldw, w_scales, ld_ws, R, N, K, out, out_dt, ld_out);
+    if (st != BNN_OK) return st;
+    if (E < 0 || ws_stride < 0 || (offsets == nullptr && E > 0 && R > 0 && N > 0)) return BNN_ERR_INVALID_ARG;
+    if (ldw > INT64_MAX / (N + 1) || w_stride < N * ldw) return BNN_ERR_INVALID_ARG;
+    if (w_stride % 16 != 0 || !aligned(offsets, 4)) return BNN_ERR_ALIGNMENT;
+    if (E > 1024) return BNN_ERR_UNSUPPORTED;
+    if (R == 0 || N == 0 || E == 0) return BNN_OK;
+    const bnn::Fp8Gemm g{A,         lda,     a_scales, ld_as,  W,      ldw,    w_stride, w_scales, ld_ws,
+                         ws_stride, offsets, (int)R,   (int)E, (int)N, (int)K, out,      ld_out};
+    return launch_fp8_gemm(g, out_dt, as_cuda(stream));
+}
+
+bnn_status bnn_route(const void* logits, bnn_dtype dt, int64_t T, int64_t E, int64_t ld,
+                     const bnn_route_params* rp, int32_t* idx, float* weights, int32_t* offsets, int32_t* row_token,
+                     int32_t* slot_row, bnn_stream_t stream) {
+    using namespace bnn::route;
+    if (rp == nullptr || !real_dtype(dt)) return BNN_ERR_INVALID_ARG;
+    const bool plan = offsets != nullptr;
+    if (T > 0 && (logits == nullptr || idx == nullptr || weights == nullptr || plan != (row_token != nullptr) ||
+                  plan != (slot_row != nullptr)))
+        return BNN_ERR_INVALID_ARG;
+    if (T < 0 || E < 1 || ld < E || rp->k < 1 || rp->k > E) return BNN_ERR_INVALID_ARG;
+    if (rp->score != BNN_ROUTE_SOFTMAX && rp->score != BNN_ROUTE_SIGMOID) return BNN_ERR_INVALID_ARG;
+    if (rp->n_groups < 1 || rp->n_groups > MAX_GROUPS || E % rp->n_groups != 0 || rp->kept_groups < 1 ||
+        rp->kept_groups > rp->n_groups || (rp->group_top != 1 && rp->group_top != 2) ||
+        (rp->renormalize != 0 && rp->renormalize != 1) || !std::isfinite(rp->scale))
+        return BNN_ERR_INVALID_ARG;
+    if (E > MAX_E || rp->k > MAX_K) return BNN_ERR_UNSUPPORTED;
+    if (T > (INT_MAX - 1024) / rp->k) return BNN_ERR_INVALID_ARG;
+    if (!aligned(logits, (uintptr_t)dtype_bytes(dt)) || !aligned(idx, 4) || !aligned(weights, 4) ||
+        !aligned(offsets, 4) || !aligned(row_token, 4) || !aligned(slot_row, 4) || !aligned(rp->bias, 4))
+        return BNN_ERR_ALIGNMENT;
+    cudaStream_t s = as_cuda(stream);
+    if (T > 0) {
+        const bnn::RouteParams p{(int)T,        (int)E,           rp->k,         ld,
+                                 rp->score,     rp->n_groups,     rp->kept_groups, rp->group_top,
+                                 rp->renormalize, rp->scale,      rp->bias,      idx,
+                                 weights};
+        if (dt == BNN_F32) launch_route_topk<float>(logits, p, s);
+        else launch_route_topk<__nv_bfloat16>(logits, p, s);
+        const bnn_status st = launch_status();
+        if (st != BNN_OK) return st;
+    }
+    if (!plan) return BNN_OK;
+    cudaLaunchConfig_t cfg{};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = PLAN_CLUSTER;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.gridDim = dim3(PLAN_CLUSTER);
+    cfg.blockDim = dim3(PLAN_THREADS);
+    cfg.dynamicSmemBytes = (size_t)(2 * MAX_E + PLAN_THREADS / 32 * E) * 4;
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, bnn::route_plan_kernel, (const int32_t*)idx, (int)(T * rp->k), (int)rp->k, (int)E,
+                           offsets, row_token, slot_row) != cudaSuccess) {
+        (void)cudaGetLastError();
+        return BNN_ERR_CUDA;
+    }
+    return launch_status();
+}
+
+bnn_status bnn_route_combine(const void* Y, bnn_dtype dt, int64_t R, int64_t N, int64_t ld_y, const int32_t* slot_row,
+                             const float* weights, int64_t T, int64_t k, void* out, bnn_dtype out_dt, int64_t ld_out,
+                             bnn_stream_t stream) {
+    if (!real_dtype(dt) || !real_dtype(out_dt)) return BNN_ERR_INVALID_ARG;
+    if (T > 0 && N > 0 && ((Y == nullptr && R > 0) || slot_row == nullptr || weights == nullptr || out == nullptr))
+        return BNN_ERR_INVALID_ARG;
+    if (R < 0 || N < 0 || T < 0 || k < 1 || ld_y < N || ld_out < N || R > kMaxDim || N > kMaxDim || T > kMaxDim)
+        return BNN_ERR_INVALID_ARG;
+    if (!aligned(Y, (uintptr_t)dtype_bytes(dt)) || !aligned(out, (uintptr_t)dtype_bytes(out_dt)) ||
+        !aligned(slot_row, 4) || !aligned(weights, 4))
+        return BNN_ERR_ALIGNMENT;
+    if (k > 64) return BNN_ERR_UNSUPPORTED;
+    if (T == 0 || N == 0) return BNN_OK;
+    cudaStream_t s = as_cuda(stream);
+    using bf16 = __nv_bfloat16;
+    if (dt == BNN_F32 && out_dt == BNN_F32)
+        launch_route_combine<float, float>(Y, R, N, ld_y, slot_row, weights, T, k, out, ld_out, s);
+    else if (dt == BNN_F32)
+        launch_route_combine<float, bf16>(Y, R, N, ld_y, slot_row, weights, T, k, out, ld_out, s);
+    else if (out_dt == BNN_F32)
+        launch_route_combine<bf16, float>(Y, R, N, ld_y, slot_row, weights, T, k, out, ld_out, s);
+    else
+        launch_route_combine<bf16, bf16>(Y, R, N, ld_y, slot_row, weights, T, k, out, ld_out, s);
     return launch_status();
 }
 
