@@ -567,6 +567,16 @@ def _same_device(*tensors: Optional[torch.Tensor]) -> None:
             raise ValueError(f"a tensor on {t.device}, with cuda:{d} as the current device")
 
 
+def _row_stride(t: torch.Tensor) -> int:
+    """Row stride of a matrix, at least its width (torch leaves the stride of a single row arbitrary)."""
+    return t.stride(-2) if t.shape[-2] > 1 else max(t.stride(-2), t.shape[-1])
+
+
+def _unit(t: torch.Tensor) -> bool:
+    """Elements of a row next to each other (a single one has any stride)."""
+    return t.stride(-1) == 1 or t.shape[-1] <= 1
+
+
 def bnn_fp8_ld_bytes(K: int) -> int:
     return int(_lib.bnn_fp8_ld_bytes(int(K)))
 
@@ -579,21 +589,16 @@ def bnn_fp8_pack(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, blo
     x_rows, Kx = x.shape
     rows = codes.shape[0]
     K = Kx if K is None else int(K)
-    if x.stride(1) != 1 or codes.stride(1) != 1 or scales.stride(1) != 1 or codes.dtype not in _CODES or \
+    if not (_unit(x) and _unit(codes) and _unit(scales)) or codes.dtype not in _CODES or \
             scales.dtype != torch.float32 or K > Kx or scales.shape[0] < (K + 127) // 128 or \
             codes.shape[1] < bnn_fp8_ld_bytes(K) or scales.shape[1] < -(-rows // int(block_rows)):
         raise ValueError("codes [rows, ld >= K rounded up to 16] and fp32 scales [blocks of K, row blocks], unit inner stride")
     if row_index is not None and (row_index.dtype != torch.int32 or tuple(row_index.shape) != (rows,) or
-                                  row_index.stride(0) != 1):
+                                  not row_index.is_contiguous()):
         raise ValueError("row_index is a contiguous int32 [rows]")
     _check("bnn_fp8_pack", _lib.bnn_fp8_pack(
         _ptr(x), _dtype(x), x_rows, K, _row_stride(x), _ptr(row_index), rows, int(block_rows), _ptr(codes),
         _row_stride(codes), _ptr(scales), _row_stride(scales), _stream(stream)))
-
-
-def _row_stride(t: torch.Tensor) -> int:
-    """Row stride of a matrix, at least its width (torch leaves the stride of a single row arbitrary)."""
-    return t.stride(-2) if t.shape[-2] > 1 else max(t.stride(-2), t.shape[-1])
 
 
 def bnn_fp8_gemm(A: torch.Tensor, a_scales: torch.Tensor, W: torch.Tensor, w_scales: torch.Tensor, K: int,
@@ -615,7 +620,7 @@ def bnn_fp8_gemm_grouped(A: torch.Tensor, a_scales: torch.Tensor, offsets: torch
     R, K = A.shape[0], int(K)
     E, N = W.shape[:2]
     _same_device(A, a_scales, offsets, W, w_scales, out)
-    if offsets.dtype != torch.int32 or tuple(offsets.shape) != (E + 1,) or offsets.stride(0) != 1 or \
+    if offsets.dtype != torch.int32 or tuple(offsets.shape) != (E + 1,) or not offsets.is_contiguous() or \
             W.dim() != 3 or w_scales.dim() != 3 or w_scales.shape[0] != E:
         raise ValueError("offsets int32 [E + 1], W [E, N, ld], w_scales [E, blocks of K, row blocks]")
     _check_fp8(A, a_scales, W, w_scales, R, N, K, out)
@@ -633,8 +638,7 @@ def _check_fp8(A, a_scales, W, w_scales, M, N, K, out) -> None:
     if A.shape[1] < ld or W.shape[-1] < ld or a_scales.shape[0] < kb or a_scales.shape[1] < M or \
             w_scales.shape[-2] < kb or w_scales.shape[-1] < (N + 127) // 128 or tuple(out.shape) != (M, N):
         raise ValueError("sizes of codes, scales and out do not fit M, N and K")
-    if A.stride(-1) != 1 or W.stride(-1) != 1 or a_scales.stride(-1) != 1 or w_scales.stride(-1) != 1 or \
-            (out.stride(-1) != 1 and N > 1):
+    if not (_unit(A) and _unit(W) and _unit(a_scales) and _unit(w_scales) and _unit(out)):
         raise ValueError("unit inner strides")
 
 
@@ -649,7 +653,7 @@ def bnn_route(logits: torch.Tensor, idx: torch.Tensor, weights: torch.Tensor, sc
     _same_device(logits, idx, weights, bias, offsets, row_token, slot_row)
     if idx.dtype != torch.int32 or weights.dtype != torch.float32 or tuple(idx.shape) != (T, k) or \
             tuple(weights.shape) != (T, k) or not idx.is_contiguous() or not weights.is_contiguous() or \
-            (logits.stride(1) != 1 and E > 1):
+            not _unit(logits):
         raise ValueError("logits [T, E] of unit inner stride, idx int32 [T, k] and weights float32 [T, k], contiguous")
     for t, n in ((offsets, E + 1), (row_token, T * k), (slot_row, T * k)):
         if t is not None and (t.dtype != torch.int32 or t.numel() != n or not t.is_contiguous()):
@@ -671,7 +675,7 @@ def bnn_route_combine(Y: torch.Tensor, slot_row: torch.Tensor, weights: torch.Te
     _same_device(Y, slot_row, weights, out)
     if slot_row.dtype != torch.int32 or weights.dtype != torch.float32 or slot_row.numel() != T * k or \
             not slot_row.is_contiguous() or not weights.is_contiguous() or tuple(out.shape) != (T, N) or \
-            (N > 1 and (Y.stride(1) != 1 or out.stride(1) != 1)):
+            not (_unit(Y) and _unit(out)):
         raise ValueError("slot_row int32 [T, k] and weights float32 [T, k], contiguous; Y [R, N], out [T, N]")
     _check("bnn_route_combine", _lib.bnn_route_combine(
         _ptr(Y), _dtype(Y), R, N, _row_stride(Y), _ptr(slot_row), _ptr(weights), T, k, _ptr(out), _dtype(out),

@@ -1729,11 +1729,169 @@ bnn_status check_fp8_product(const uint8_t* A, int64_t lda, const float* sa, int
     return BNN_OK;
 }
 
-bnn_status launch_fp8_gemm(const bnn::Fp8Gemm& g, int out_dt, cudaStream_t stream) {
-    const dim3 grid((unsigned)ceil_div(g.N, 64), (unsigned)ceil_div(g.R, 64), (unsigned)g.E);
-    if (out_dt == BNN_F32) bnn::fp8_gemm_simple_kernel<float><<<grid, 256, 0, stream>>>(g);
-    else bnn::fp8_gemm_simple_kernel<__nv_bfloat16><<<grid, 256, 0, stream>>>(g);
+// Tensor maps of e4m3 codes: 128 bytes of K x box_rows, 128-byte swizzle, zero
+// fill past K and past the rows (of each group for W).
+bool encode_fp8_map(CUtensorMap* map, const uint8_t* base, int64_t K, int64_t rows, int64_t ld, int64_t groups,
+                    int64_t stride, int box_rows) {
+    auto enc = tensor_map_encoder();
+    if (enc == nullptr) return false;
+    const cuuint32_t rank = groups > 0 ? 3 : 2;
+    cuuint64_t dims[3] = {(cuuint64_t)K, (cuuint64_t)rows, (cuuint64_t)groups};
+    cuuint64_t strides[2] = {(cuuint64_t)ld, (cuuint64_t)stride};
+    cuuint32_t box[3] = {(cuuint32_t)bnn::fp8::BLOCK, (cuuint32_t)box_rows, 1};
+    cuuint32_t estr[3] = {1, 1, 1};
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, rank, const_cast<uint8_t*>(base), dims, strides, box, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Per-device one-time opt-in of the 8-bit kernels to their shared memory; the
+// number of CTA pairs that fit on the device at once, or -1.
+template <int NT>
+bool fp8_split_opt_in() {
+    constexpr int bytes = bnn::f8s::Cfg<NT>::SMEM_BYTES;
+    return cudaFuncSetAttribute(bnn::fp8_gemm_split_kernel<NT, float>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                bytes) == cudaSuccess &&
+           cudaFuncSetAttribute(bnn::fp8_gemm_split_kernel<NT, __nv_bfloat16>,
+                                cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) == cudaSuccess;
+}
+template <int BN>
+bool fp8_pair_opt_in() {
+    constexpr int bytes = bnn::f8p::Cfg<BN>::SMEM_BYTES;
+    return cudaFuncSetAttribute(bnn::fp8_gemm_pair_kernel<BN, float>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                bytes) == cudaSuccess &&
+           cudaFuncSetAttribute(bnn::fp8_gemm_pair_kernel<BN, __nv_bfloat16>,
+                                cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) == cudaSuccess;
+}
+int fp8_pairs_resident() {
+    constexpr int kMaxDevices = 64;
+    static std::atomic<int> pairs[kMaxDevices];              // 0: not configured yet
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0) return -1;
+    if (dev < kMaxDevices) {
+        const int p = pairs[dev].load(std::memory_order_acquire);
+        if (p > 0) return p;
+    }
+    if (!fp8_split_opt_in<16>() || !fp8_split_opt_in<32>() || !fp8_split_opt_in<64>() || !fp8_split_opt_in<128>() ||
+        !fp8_pair_opt_in<128>() || !fp8_pair_opt_in<256>())
+        return -1;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.gridDim = dim3(2 * 74);
+    cfg.blockDim = dim3(bnn::f8p::THREADS);
+    cfg.dynamicSmemBytes = bnn::f8p::Cfg<256>::SMEM_BYTES;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, bnn::fp8_gemm_pair_kernel<256, __nv_bfloat16>, &cfg) != cudaSuccess || n < 1) {
+        (void)cudaGetLastError();
+        return -1;
+    }
+    if (dev < kMaxDevices) pairs[dev].store(n, std::memory_order_release);
+    return n;
+}
+
+// A launch in clusters of `cluster` CTAs with programmatic dependent launch:
+// the kernels' set-up may overlap the previous kernel.
+template <typename Kernel, typename... Args>
+bnn_status launch_clusters(Kernel kernel, dim3 grid, int threads, int smem, int cluster, cudaStream_t stream,
+                           Args... args) {
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)cluster;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = (size_t)smem;
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    if (cudaLaunchKernelEx(&cfg, kernel, args...) != cudaSuccess) {
+        (void)cudaGetLastError();
+        return BNN_ERR_CUDA;
+    }
     return launch_status();
+}
+
+struct Fp8Operands {
+    const uint8_t *A, *W;
+    int64_t lda, ldw, w_stride;
+};
+
+template <int NT, typename T>
+bnn_status launch_fp8_split(const Fp8Operands& o, const bnn::Fp8Gemm& g, int64_t chunks, cudaStream_t stream) {
+    using C = bnn::f8s::Cfg<NT>;
+    CUtensorMap tmA, tmW;
+    if (!encode_fp8_map(&tmA, o.A, g.K, g.R, o.lda, 0, 0, NT) ||
+        !encode_fp8_map(&tmW, o.W, g.K, g.N, o.ldw, g.E, o.w_stride, bnn::f8s::BN))
+        return BNN_ERR_CUDA;
+    const int64_t tiles_n = ceil_div(g.N, bnn::f8s::BN), tiles = tiles_n * g.E;
+    const int64_t nk = ceil_div(g.K, bnn::fp8::BLOCK);
+    // Split of K: as many CTAs as fill the SMs twice, at the fewest K blocks a
+    // CTA has to take one after the other (plus about four blocks' time to
+    // start and to add the parts).
+    const int64_t slots = 2 * (int64_t)sm_count();
+    int S = 1;
+    int64_t best = INT64_MAX;
+    for (int s = 1; s <= bnn::f8s::MAX_SPLIT && s <= nk; ++s) {
+        const int64_t cost = ceil_div(tiles * chunks * s, slots) * (ceil_div(nk, s) + 4);
+        if (cost < best) {
+            best = cost;
+            S = s;
+        }
+    }
+    return launch_clusters(bnn::fp8_gemm_split_kernel<NT, T>, dim3((unsigned)(tiles * S), (unsigned)chunks),
+                           bnn::f8s::THREADS, C::SMEM_BYTES, S, stream, tmA, tmW, g, (int)tiles_n, S);
+}
+
+template <int BN, typename T>
+bnn_status launch_fp8_pair(const Fp8Operands& o, const bnn::Fp8Gemm& g, int64_t tiles, int pairs, cudaStream_t stream) {
+    using C = bnn::f8p::Cfg<BN>;
+    CUtensorMap tmA, tmW;
+    if (!encode_fp8_map(&tmA, o.A, g.K, g.R, o.lda, 0, 0, bnn::f8p::BM) ||
+        !encode_fp8_map(&tmW, o.W, g.K, g.N, o.ldw, g.E, o.w_stride, BN / 2))
+        return BNN_ERR_CUDA;
+    const int vec = aligned(g.out, 16) && g.ldo * (int64_t)sizeof(T) % 16 == 0 ? 1 : 0;
+    return launch_clusters(bnn::fp8_gemm_pair_kernel<BN, T>, dim3((unsigned)(2 * std::min<int64_t>(tiles, pairs))),
+                           bnn::f8p::THREADS, C::SMEM_BYTES, 2, stream, tmA, tmW, g, vec);
+}
+
+template <typename T>
+bnn_status launch_fp8_gemm_as(const Fp8Operands& o, const bnn::Fp8Gemm& g, cudaStream_t stream) {
+    const int pairs = fp8_pairs_resident();
+    if (pairs < 0) return BNN_ERR_CUDA;
+    // Rows that a group has to expect (all of them without groups): the counts
+    // themselves are on the device.
+    const int64_t rows = ceil_div(g.R, g.E);
+    const bool grouped = g.offsets != nullptr;
+    if (ceil_div(g.N, 128) * g.E > (1 << 27) || (ceil_div(g.R, 256) + g.E) * ceil_div(g.N, 128) > (1 << 30))
+        return BNN_ERR_UNSUPPORTED;
+    if (rows <= 128) {
+        const int64_t chunks = 1;
+        if (rows <= 16) return launch_fp8_split<16, T>(o, g, chunks, stream);
+        if (rows <= 32) return launch_fp8_split<32, T>(o, g, chunks, stream);
+        if (rows <= 64) return launch_fp8_split<64, T>(o, g, chunks, stream);
+        return launch_fp8_split<128, T>(o, g, chunks, stream);
+    }
+    const int64_t tiles_m = grouped ? ceil_div(g.R, 256) + g.E / 2 : ceil_div(g.R, 256);
+    const int64_t t256 = tiles_m * ceil_div(g.N, 256), t128 = tiles_m * ceil_div(g.N, 128);
+    if (ceil_div(t256, pairs) * 2 <= ceil_div(t128, pairs)) return launch_fp8_pair<256, T>(o, g, t256, pairs, stream);
+    return launch_fp8_pair<128, T>(o, g, t128, pairs, stream);
+}
+
+bnn_status launch_fp8_gemm(const Fp8Operands& o, const bnn::Fp8Gemm& g, int out_dt, cudaStream_t stream) {
+    constexpr int64_t kMaxStride = (int64_t)1 << 40;          // of a tensor map, in bytes
+    if (o.lda >= kMaxStride || o.ldw >= kMaxStride || o.w_stride >= kMaxStride) return BNN_ERR_UNSUPPORTED;
+    return out_dt == BNN_F32 ? launch_fp8_gemm_as<float>(o, g, stream)
+                             : launch_fp8_gemm_as<__nv_bfloat16>(o, g, stream);
 }
 
 template <typename T, int ALIGN>
@@ -1820,9 +1978,8 @@ bnn_status bnn_fp8_gemm(const uint8_t* A, int64_t lda, const float* a_scales, in
         check_fp8_product(A, lda, a_scales, ld_as, W, ldw, w_scales, ld_ws, M, N, K, out, out_dt, ld_out);
     if (st != BNN_OK) return st;
     if (M == 0 || N == 0) return BNN_OK;
-    const bnn::Fp8Gemm g{A,  lda,  a_scales, ld_as, W,   ldw,     0,       w_scales, ld_ws,
-                         0,  nullptr, (int)M, 1,    (int)N, (int)K, out, ld_out};
-    return launch_fp8_gemm(g, out_dt, as_cuda(stream));
+    const bnn::Fp8Gemm g{a_scales, ld_as, w_scales, ld_ws, 0, nullptr, (int)M, 1, (int)N, (int)K, out, ld_out};
+    return launch_fp8_gemm(Fp8Operands{A, W, lda, ldw, ldw}, g, out_dt, as_cuda(stream));
 }
 
 bnn_status bnn_fp8_gemm_grouped(const uint8_t* A, int64_t lda, const float* a_scales, int64_t ld_as, int64_t R,
@@ -1837,9 +1994,9 @@ bnn_status bnn_fp8_gemm_grouped(const uint8_t* A, int64_t lda, const float* a_sc
     if (w_stride % 16 != 0 || !aligned(offsets, 4)) return BNN_ERR_ALIGNMENT;
     if (E > 1024) return BNN_ERR_UNSUPPORTED;
     if (R == 0 || N == 0 || E == 0) return BNN_OK;
-    const bnn::Fp8Gemm g{A,         lda,     a_scales, ld_as,  W,      ldw,    w_stride, w_scales, ld_ws,
-                         ws_stride, offsets, (int)R,   (int)E, (int)N, (int)K, out,      ld_out};
-    return launch_fp8_gemm(g, out_dt, as_cuda(stream));
+    const bnn::Fp8Gemm g{a_scales, ld_as,  w_scales, ld_ws,  ws_stride, offsets,
+                         (int)R,   (int)E, (int)N,   (int)K, out,       ld_out};
+    return launch_fp8_gemm(Fp8Operands{A, W, lda, ldw, w_stride}, g, out_dt, as_cuda(stream));
 }
 
 bnn_status bnn_route(const void* logits, bnn_dtype dt, int64_t T, int64_t E, int64_t ld,

@@ -1,21 +1,33 @@
 // Products of 8-bit floating-point operands with block scales (fp8.cuh):
 //   C[m, n] = sum_b sA[b, m] sW[b, n / 128] sum_{k in block b} a[m, k] w[n, k]
-// with every block's inner sum and the outer sum in fp32.
+//
+// The inner sum of a block is four tcgen05.mma kind::f8f6f4 (K = 32 each) into
+// a fresh fp32 accumulator in tensor memory; the sum over blocks is kept in
+// fp32 registers, C += s * inner, because every block has its own scale.  K
+// tails need no care: the tensor maps end at K, so the copies fill zeros.
+//
+// Two kernels share the work:
+//  * fp8_gemm_split_kernel, few rows: the weights are the 128-row operand of
+//    the MMA and the rows of A its N (16 .. 128), so that a small batch wastes
+//    nothing; K is split over a cluster.
+//  * fp8_gemm_pair_kernel, many rows: CTA pairs on 256 rows x 128 or 256
+//    columns.
+// Every mbarrier wait is bounded as in gemm_tc.cuh: on time-out the roles stop
+// at their next wait, outstanding copies and MMAs are waited for (bounded),
+// and tensor memory is freed before exit.
 #pragma once
 
 #include "fp8.cuh"
+#include "gemm_f4.cuh"
 
 namespace bnn {
 
 // Operands of a (grouped) product.  Dense: offsets == nullptr, one group of R
-// rows.  Grouped: rows offsets[e] .. offsets[e + 1] of A meet W[e].
+// rows.  Grouped: rows offsets[e] .. offsets[e + 1] of A meet W[e].  A and W
+// themselves come through tensor maps.
 struct Fp8Gemm {
-    const uint8_t* A;
-    int64_t lda;
     const float* sa;
     int64_t ldsa;
-    const uint8_t* W;
-    int64_t ldw, w_stride;
     const float* sw;
     int64_t ldsw, sw_stride;
     const int32_t* offsets;
@@ -31,65 +43,607 @@ __device__ __forceinline__ float fp8_out<float>(float v) { return v; }
 template <>
 __device__ __forceinline__ __nv_bfloat16 fp8_out<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
 
-__device__ __forceinline__ float fp8_value(uint8_t c) {
-    __nv_fp8_e4m3 t;
-    t.__x = c;
-    return (float)t;
+// Rows [r0, r1) of group e, clamped to [0, R] whatever the offsets hold.
+__device__ __forceinline__ int2 fp8_group_rows(const Fp8Gemm& g, int e) {
+    if (g.offsets == nullptr) return make_int2(0, g.R);
+    const int r0 = max(0, min(g.offsets[e], g.R));
+    return make_int2(r0, max(r0, min(g.offsets[e + 1], g.R)));
 }
 
-// 64 x 64 outputs per CTA, 4 x 4 per thread, operands decoded to fp32 in
-// shared memory 32 columns of K at a time.
-template <typename T>
-__global__ void __launch_bounds__(256) fp8_gemm_simple_kernel(Fp8Gemm g) {
-    constexpr int KC = 32;
-    __shared__ float as[KC][64 + 4], ws[KC][64 + 4];
-    const int e = blockIdx.z;
-    int r0 = 0, r1 = g.R;
-    if (g.offsets != nullptr) {
-        r0 = max(0, min(g.offsets[e], g.R));
-        r1 = max(r0, min(g.offsets[e + 1], g.R));
+template <int CTAS>
+__device__ __forceinline__ void mma_f8(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                       uint32_t accumulate) {
+    if constexpr (CTAS == 2) {
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "setp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+            "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+            : "memory");
+    } else {
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "setp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+            "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+            : "memory");
     }
-    const int m0 = r0 + blockIdx.y * 64, n0 = blockIdx.x * 64;
-    if (m0 >= r1) return;
-    const uint8_t* W = g.W + e * g.w_stride;
-    const float* sw = g.sw + e * g.sw_stride;
-    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-    float y[4][4] = {};
-    for (int kb = 0; kb * fp8::BLOCK < g.K; ++kb) {
-        float p[4][4] = {};
-        for (int k0 = kb * fp8::BLOCK; k0 < min(g.K, (kb + 1) * fp8::BLOCK); k0 += KC) {
-            __syncthreads();
-            for (int i = threadIdx.x; i < 64 * KC; i += 256) {
-                const int r = i / KC, k = k0 + i % KC;
-                as[i % KC][r] = m0 + r < r1 && k < g.K ? fp8_value(g.A[(int64_t)(m0 + r) * g.lda + k]) : 0.0f;
-                ws[i % KC][r] = n0 + r < g.N && k < g.K ? fp8_value(W[(int64_t)(n0 + r) * g.ldw + k]) : 0.0f;
-            }
-            __syncthreads();
-            for (int k = 0; k < KC; ++k) {
-                #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    #pragma unroll
-                    for (int j = 0; j < 4; ++j) p[i][j] = fmaf(as[k][ty * 4 + i], ws[k][tx * 4 + j], p[i][j]);
+}
+
+// kind::f8f6f4 instruction descriptor: D fp32 (bits 4-5 = 1), A and B e4m3
+// (0 at bits 7-9 and 10-12), both K-major, N >> 3 at bits 17-22, M >> 4 at 24-28.
+__host__ __device__ constexpr uint32_t f8_idesc(int m, int n) {
+    return (1u << 4) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
+}
+
+// acc += t * s on pairs of fp32 (one instruction per two products).
+__device__ __forceinline__ void fma2(float2& acc, float2 t, float2 s) {
+    asm("fma.rn.f32x2 %0, %1, %2, %0;"
+        : "+l"(reinterpret_cast<unsigned long long&>(acc))
+        : "l"(reinterpret_cast<unsigned long long&>(t)), "l"(reinterpret_cast<unsigned long long&>(s)));
+}
+
+__device__ __forceinline__ float ld_shared_cluster_f32(uint32_t addr) {
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+    return v;
+}
+__device__ __forceinline__ uint32_t mapa_shared(uint32_t addr, uint32_t rank) {
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+    return r;
+}
+
+// ---------------------------------------------------------------------------
+// Few rows: out^T tile of 128 weight rows x NT rows of A per cluster.
+// ---------------------------------------------------------------------------
+namespace f8s {
+constexpr int BN = 128;                      // weight rows per CTA = TMEM lanes
+constexpr int W_BYTES = BN * fp8::BLOCK;     // 16 KiB of weights per stage
+constexpr int WARP_PRODUCER = 0, WARP_MMA = 1, WARP_EPI0 = 2;
+constexpr int THREADS = 6 * 32;
+constexpr int MAX_SPLIT = 8;
+// Two CTAs share an SM: weights stream from HBM while the other CTA starts or
+// ends.  Never three, so that two always find their tensor memory (see NBUF):
+// a cluster's CTAs wait for one another and must not wait for an allocation.
+constexpr int SMEM_TWO = 113 * 1024;
+template <int NT>
+struct Cfg {
+    static constexpr int STAGE = W_BYTES + NT * fp8::BLOCK;
+    static constexpr int FIXED = 2 * NT * 4 + 512 + 1024;
+    static constexpr int STAGES = (SMEM_TWO - FIXED) / STAGE;
+    static constexpr int SMEM_BYTES = FIXED + STAGES * STAGE;
+    // Accumulators in flight; with two CTAs per SM they fill at most 512 columns.
+    static constexpr int NBUF = NT <= 64 ? 4 : 2;
+    static constexpr int TMEM_COLS = NBUF * NT < 32 ? 32 : NBUF * NT;
+    static_assert(STAGES >= 3 && TMEM_COLS <= 256, "two CTAs per SM");
+    static_assert(3 * (SMEM_BYTES + 1024) > 228 * 1024, "never three CTAs per SM");
+    static_assert(NT * BN * 4 <= STAGES * STAGE, "the partial sums reuse the ring");
+    static_assert(STAGE % 1024 == 0, "128B swizzle");
+    static_assert((2 * STAGES + 2 * NBUF + 1) * 8 + 16 <= 512, "barriers");
+};
+}  // namespace f8s
+
+// grid: (tiles of 128 weight rows x E) * S CTAs in clusters of S, y over chunks
+// of NT rows (a group's chunks are walked in steps of gridDim.y).  Cluster
+// rank r takes K blocks [r nk / S, (r + 1) nk / S).
+//  warp 0     producer: TMA of 128 weight rows and NT rows of A per K block.
+//  warp 1     one thread issues the block's four MMAs (M = 128, N = NT) and
+//             commits them to the stage and to the accumulator.
+//  warps 2-5  epilogue: thread = one weight row; per block NT accumulators
+//             from tensor memory times sA[b, column] * sW[b, tile], the
+//             products of scales passing through shared memory one block ahead.
+// With S > 1 the CTAs leave their partial sums in shared memory and each adds
+// the columns r, r + S, ... of all of them in rank order: the same sum on every run.
+template <int NT, typename T>
+__global__ void __launch_bounds__(f8s::THREADS)
+fp8_gemm_split_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmW, Fp8Gemm g,
+                      int tiles_n, int S) {
+    using namespace f8s;
+    using C = Cfg<NT>;
+    constexpr int STAGES = C::STAGES, NBUF = C::NBUF;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* ring = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    float* sbuf = reinterpret_cast<float*>(ring + STAGES * C::STAGE);      // [2][NT]
+    uint64_t* full = reinterpret_cast<uint64_t*>(sbuf + 2 * NT);
+    uint64_t* empty = full + STAGES;
+    uint64_t* tfull = empty + STAGES;
+    uint64_t* tempty = tfull + NBUF;
+    uint64_t* drain = tempty + NBUF;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int cid = (int)blockIdx.x / S, rank = (int)blockIdx.x % S;
+    const int e = cid / tiles_n, tile = cid % tiles_n, n0 = tile * BN;
+    const int nk = (g.K + fp8::BLOCK - 1) / fp8::BLOCK;
+    const int kb0 = (int)((int64_t)rank * nk / S), kb1 = (int)((int64_t)(rank + 1) * nk / S);
+
+    if (threadIdx.x == 0) {
+        prefetch_tensormap(&tmA);
+        prefetch_tensormap(&tmW);
+        for (int s = 0; s < STAGES; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&empty[s], 1);
+        }
+        for (int b = 0; b < NBUF; ++b) {
+            mbar_init(&tfull[b], 1);
+            mbar_init(&tempty[b], 4);
+        }
+        mbar_init(drain, 1);
+        *abort_flag = 0;
+        fence_mbarrier_init();
+    }
+    if (warp == WARP_MMA) {
+        tmem_alloc(tmem_slot, C::TMEM_COLS);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem_base = *tmem_slot;
+    // Everything above may overlap the previous kernel; operands, offsets and
+    // outputs are touched only after it.
+    grid_dependency_wait();
+    grid_dependents_launch();
+    const int2 rows = fp8_group_rows(g, e);
+
+    uint32_t it = 0;                          // K blocks this role has handled, over all chunks
+    uint32_t issued = 0;
+    bool ok = true;
+    for (int m0 = rows.x + (int)blockIdx.y * NT; m0 < rows.y; m0 += (int)gridDim.y * NT) {
+        if (warp == WARP_PRODUCER) {
+            if (lane == 0) {
+                for (int kb = kb0; ok && kb < kb1; ++kb, ++it) {
+                    const uint32_t s = it % STAGES;
+                    if (it >= STAGES && !tc_wait(&empty[s], ((it / STAGES) - 1) & 1, abort_flag)) {
+                        ok = false;
+                        break;
+                    }
+                    uint8_t* dst = ring + s * C::STAGE;
+                    mbar_arrive_expect_tx(&full[s], C::STAGE);
+                    tma_load_3d(dst, &tmW, kb * fp8::BLOCK, n0, e, &full[s]);
+                    tma_load_2d(dst + W_BYTES, &tmA, kb * fp8::BLOCK, m0, &full[s]);
+                    ++issued;
                 }
             }
-        }
-        #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int m = min(m0 + ty * 4 + i, r1 - 1);
-            const int n = min(n0 + tx * 4, g.N - 1);
-            const float s = g.sa[kb * g.ldsa + m] * sw[kb * g.ldsw + n / fp8::BLOCK];
+            __syncwarp();
+        } else if (warp == WARP_MMA) {
+            if (lane == 0) {
+                for (int kb = kb0; ok && kb < kb1; ++kb, ++it) {
+                    const uint32_t s = it % STAGES, b = it % NBUF;
+                    if ((it >= NBUF && !tc_wait(&tempty[b], ((it / NBUF) - 1) & 1, abort_flag)) ||
+                        !tc_wait(&full[s], (it / STAGES) & 1, abort_flag)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t w = smem_u32(ring + s * C::STAGE), a = w + W_BYTES;
+                    #pragma unroll
+                    for (int kk = 0; kk < 4; ++kk)
+                        mma_f8<1>(tmem_base + b * NT, umma_desc_sw128(w + kk * 32), umma_desc_sw128(a + kk * 32),
+                                  f8_idesc(BN, NT), kk != 0 ? 1u : 0u);
+                    mma_commit(&empty[s]);
+                    mma_commit(&tfull[b]);
+                }
+            }
+            __syncwarp();
+        } else {
+            const int quad = warp & 3, tid = (int)threadIdx.x - WARP_EPI0 * 32;
+            const int cols = min(NT, rows.y - m0);
+            const bool mine = tid < cols;
+            const float* sa = g.sa + m0 + tid;
+            const float* sw = g.sw + e * g.sw_stride + tile;
+            auto scale = [&](int kb) { return mine && kb < kb1 ? sa[kb * g.ldsa] * sw[kb * g.ldsw] : 0.0f; };
+            float2 acc[NT / 2];
             #pragma unroll
-            for (int j = 0; j < 4; ++j) y[i][j] = fmaf(p[i][j], s, y[i][j]);
+            for (int c = 0; c < NT / 2; ++c) acc[c] = make_float2(0.0f, 0.0f);
+            if (tid < NT) sbuf[tid] = scale(kb0);
+            float next = scale(kb0 + 1);
+            named_bar_sync(f4::EPI_BAR, 128);
+            for (int kb = kb0; kb < kb1; ++kb, ++it) {
+                const uint32_t b = it % NBUF;
+                const float* s = sbuf + ((kb - kb0) & 1) * NT;
+                ok = ok && __all_sync(0xffffffffu, tc_wait(&tfull[b], (it / NBUF) & 1, abort_flag));
+                if (ok) {
+                    tc_fence_after();
+                    const uint32_t t0 = tmem_base + ((uint32_t)(32 * quad) << 16) + b * NT;
+                    constexpr int CH = NT < 32 ? 16 : 32;
+                    #pragma unroll
+                    for (int c = 0; c < NT; c += CH) {
+                        uint32_t r[CH];
+                        if constexpr (CH == 16) tmem_ld16_sync(t0 + c, r);
+                        else tmem_ld32_sync(t0 + c, r);
+                        if (c + CH == NT) {
+                            tc_fence_before();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(&tempty[b]);
+                        }
+                        #pragma unroll
+                        for (int j = 0; j < CH; j += 4) {
+                            const float4 f = *reinterpret_cast<const float4*>(s + c + j);
+                            fma2(acc[(c + j) / 2], make_float2(__uint_as_float(r[j]), __uint_as_float(r[j + 1])),
+                                 make_float2(f.x, f.y));
+                            fma2(acc[(c + j) / 2 + 1],
+                                 make_float2(__uint_as_float(r[j + 2]), __uint_as_float(r[j + 3])),
+                                 make_float2(f.z, f.w));
+                        }
+                    }
+                }
+                if (tid < NT) sbuf[((kb - kb0 + 1) & 1) * NT + tid] = next;
+                next = scale(kb + 2);
+                named_bar_sync(f4::EPI_BAR, 128);
+            }
+            const int n = 32 * quad + lane;
+            T* out = static_cast<T*>(g.out) + n0 + n;
+            if (S == 1) {
+                if (ok && n0 + n < g.N) {
+                    #pragma unroll
+                    for (int c = 0; c < NT; ++c)
+                        if (c < cols) out[(int64_t)(m0 + c) * g.ldo] = fp8_out<T>(c & 1 ? acc[c / 2].y : acc[c / 2].x);
+                }
+            } else {
+                // All MMAs of this chunk are done (their accumulators were
+                // read), so the ring is free for the partial sums.
+                float* part = reinterpret_cast<float*>(ring);
+                #pragma unroll
+                for (int c = 0; c < NT; ++c) part[c * BN + n] = c & 1 ? acc[c / 2].y : acc[c / 2].x;
+            }
+        }
+        if (S > 1) {
+            __syncwarp();
+            cluster_sync_all();
+            if (warp >= WARP_EPI0) {
+                const int n = (int)threadIdx.x - WARP_EPI0 * 32, cols = min(NT, rows.y - m0);
+                T* out = static_cast<T*>(g.out) + n0 + n;
+                for (int c = rank; c < cols; c += S) {
+                    float v[MAX_SPLIT];
+                    #pragma unroll
+                    for (int r = 0; r < MAX_SPLIT; ++r)
+                        v[r] = r < S ? ld_shared_cluster_f32(mapa_shared(smem_u32(ring) + (c * BN + n) * 4, r)) : 0.0f;
+                    float y = v[0];
+                    #pragma unroll
+                    for (int r = 1; r < MAX_SPLIT; ++r) y += v[r];
+                    if (ok && n0 + n < g.N) out[(int64_t)(m0 + c) * g.ldo] = fp8_out<T>(y);
+                }
+                // Ordered before the next chunk's copies into the ring.
+                fence_proxy_async_shared();
+            }
+            __syncwarp();
+            cluster_sync_all();
         }
     }
-    T* out = static_cast<T*>(g.out);
-    #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    if (warp == WARP_PRODUCER && lane == 0 && !ok) {
+        for (uint32_t q = issued > STAGES ? issued - STAGES : 0; q < issued; ++q)
+            if (!mbar_wait_bounded(&full[q % STAGES], (q / STAGES) & 1)) break;
+    }
+    if (warp == WARP_MMA && lane == 0) {
+        mma_commit(drain);
+        mbar_wait_bounded(drain, 0);
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    if (warp == WARP_MMA) {
+        tc_fence_after();
+        tmem_dealloc(tmem_base, C::TMEM_COLS);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Many rows: CTA pairs on tiles of 256 rows x BN columns.
+// ---------------------------------------------------------------------------
+namespace f8p {
+constexpr int BM = 128;                      // rows of A per CTA = TMEM lanes
+constexpr int A_BYTES = BM * fp8::BLOCK;     // 16 KiB per stage
+constexpr int WARP_PRODUCER = 0, WARP_MMA = 1, WARP_EPI0 = 2, EPI_WARPS = 8;
+constexpr int THREADS = (WARP_EPI0 + EPI_WARPS) * 32;
+constexpr int OUT_BLOCK = 32 * 128;          // staging per epilogue warp: 32 rows x 128 bytes
+constexpr int BAND = 8;                      // row tiles that a band of concurrent tiles spans
+template <int BN>
+struct Cfg {
+    static constexpr int W_BYTES = BN / 2 * fp8::BLOCK;      // this CTA's half of the weight rows
+    static constexpr int STAGE = A_BYTES + W_BYTES;
+    static constexpr int FIXED = EPI_WARPS * OUT_BLOCK + 512 + 1024;
+    static constexpr int STAGES = (tc::SMEM_LIMIT - FIXED) / STAGE;
+    static constexpr int SMEM_BYTES = FIXED + STAGES * STAGE;
+    static constexpr int NBUF = 512 / BN;                    // accumulators in tensor memory
+    static_assert((2 * STAGES + 2 * NBUF + 1) * 8 + 16 <= 512, "barriers");
+    static_assert(STAGE % 1024 == 0, "128B swizzle");
+};
+}  // namespace f8p
+
+// TMA load into this CTA's shared memory whose bytes count on the barrier at
+// the same offset in the pair's even CTA.
+__device__ __forceinline__ void tma_load_2d_pair(void* dst, const CUtensorMap* map, int32_t x, int32_t y,
+                                                 uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3}], [%4];" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
+        : "memory");
+}
+__device__ __forceinline__ void tma_load_3d_pair(void* dst, const CUtensorMap* map, int32_t x, int32_t y, int32_t z,
+                                                 uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
+        : "memory");
+}
+
+// Where a tile lies: group, first row, first column.
+struct Fp8Tile {
+    int e, m0, n0, r1;
+};
+
+// Walks the tiles of all groups in order.  A whole warp holds a window of 32
+// groups, one per lane, with the running sum of their tiles; t grows from call
+// to call, so the window only moves forward.
+template <int BN>
+struct Fp8Tiles {
+    int tiles_n, first, base, incl;          // window's first group, tiles before it, this lane's inclusive sum
+    int2 rows;
+    __device__ __forceinline__ void load(const Fp8Gemm& g, int lane) {
+        rows = make_int2(0, 0);
+        if (first + lane < g.E) rows = fp8_group_rows(g, first + lane);
+        incl = (rows.y - rows.x + 2 * f8p::BM - 1) / (2 * f8p::BM) * tiles_n;
         #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int m = m0 + ty * 4 + i, n = n0 + tx * 4 + j;
-            if (m < r1 && n < g.N) out[(int64_t)m * g.ldo + n] = fp8_out<T>(y[i][j]);
+        for (int off = 1; off < 32; off <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, incl, off);
+            if (lane >= off) incl += y;
         }
+    }
+    __device__ __forceinline__ void init(const Fp8Gemm& g, int lane) {
+        tiles_n = (g.N + BN - 1) / BN;
+        first = base = 0;
+        load(g, lane);
+    }
+    // False past the last tile.  The whole warp calls it.
+    __device__ __forceinline__ bool find(const Fp8Gemm& g, int lane, int t, Fp8Tile& out) {
+        while (true) {
+            const int total = __shfl_sync(0xffffffffu, incl, 31);
+            if (t < base + total) break;
+            base += total;
+            first += 32;
+            if (first >= g.E) return false;
+            load(g, lane);
+        }
+        const int j = __ffs(__ballot_sync(0xffffffffu, t < base + incl)) - 1;
+        const int r0 = __shfl_sync(0xffffffffu, rows.x, j), r1 = __shfl_sync(0xffffffffu, rows.y, j);
+        const int before = __shfl_sync(0xffffffffu, incl, j > 0 ? j - 1 : 0);
+        const int lt = t - base - (j > 0 ? before : 0);
+        // Bands of BAND row tiles, column by column: the tiles in flight span
+        // about as many rows as columns and share operands in L2.
+        const int tiles_m = (r1 - r0 + 2 * f8p::BM - 1) / (2 * f8p::BM);
+        const int band = lt / (f8p::BAND * tiles_n), in = lt - band * (f8p::BAND * tiles_n);
+        const int mt = min(f8p::BAND, tiles_m - band * f8p::BAND);
+        out.e = first + j;
+        out.m0 = r0 + (band * f8p::BAND + in % mt) * (2 * f8p::BM);
+        out.n0 = in / mt * BN;
+        out.r1 = r1;
+        return true;
+    }
+};
+
+// Persistent pairs of CTAs (cta_group::2), one CTA per SM:
+//  warp 0     producer in each CTA: its 128 rows of A and its half of the BN
+//             weight rows per K block, counted on the even CTA's barrier.
+//  warp 1     in the even CTA one thread issues the four MMAs of a K block
+//             (M = 256, N = BN) for both.
+//  warps 2-9  epilogue: warp quadrants of 32 rows, two warps per quadrant with
+//             half of the columns each; thread = one row, BN / 2 fp32 sums in
+//             registers, C += (sA[b, row] * sW[b, column block]) * inner.  Half
+//             a tile lies in one column block, so the factor is one number per
+//             thread and block, loaded two blocks ahead.
+// The tensor memory holds 512 / BN accumulators: the MMAs of the next blocks
+// run while the epilogue adds this one.  The finished tile is rounded, put
+// into shared memory (16-byte chunks swizzled by row, no bank conflicts) and
+// stored in whole 128-byte lines by row, rows and columns outside left out.
+template <int BN, typename T>
+__global__ void __launch_bounds__(f8p::THREADS, 1)
+fp8_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmW, Fp8Gemm g,
+                     int vec_out) {
+    using namespace f8p;
+    using C = Cfg<BN>;
+    constexpr int STAGES = C::STAGES, NBUF = C::NBUF, HN = BN / 2;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* ring = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    uint8_t* oring = ring + STAGES * C::STAGE;
+    uint64_t* full = reinterpret_cast<uint64_t*>(oring + EPI_WARPS * OUT_BLOCK);
+    uint64_t* empty = full + STAGES;
+    uint64_t* tfull = empty + STAGES;
+    uint64_t* tempty = tfull + NBUF;
+    uint64_t* drain = tempty + NBUF;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_ctarank();
+    const int cid = (int)blockIdx.x / 2, ncl = (int)gridDim.x / 2;
+    const int nk = (g.K + fp8::BLOCK - 1) / fp8::BLOCK;
+
+    if (threadIdx.x == 0) {
+        prefetch_tensormap(&tmA);
+        prefetch_tensormap(&tmW);
+        for (int s = 0; s < STAGES; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&empty[s], 1);
+        }
+        for (int b = 0; b < NBUF; ++b) {
+            mbar_init(&tfull[b], 1);
+            mbar_init(&tempty[b], EPI_WARPS * 2);
+        }
+        mbar_init(drain, 1);
+        *abort_flag = 0;
+        fence_mbarrier_init();
+    }
+    if (warp == WARP_MMA) f4_tmem_alloc<true>(tmem_slot, 512);
+    tc_fence_before();
+    cluster_sync_all();
+    tc_fence_after();
+    const uint32_t tmem_base = *tmem_slot;
+    grid_dependency_wait();
+    grid_dependents_launch();
+
+    Fp8Tiles<BN> tiles;
+    tiles.init(g, lane);
+    Fp8Tile tl;
+    uint32_t it = 0;
+    bool ok = true;
+    if (warp == WARP_PRODUCER) {
+        uint32_t issued = 0;
+        for (int t = cid; ok && tiles.find(g, lane, t, tl); t += ncl) {
+            if (lane == 0) {
+                for (int kb = 0; kb < nk; ++kb, ++it) {
+                    const uint32_t s = it % STAGES;
+                    if (it >= STAGES && !tc_wait(&empty[s], ((it / STAGES) - 1) & 1, abort_flag)) {
+                        ok = false;
+                        break;
+                    }
+                    uint8_t* dst = ring + s * C::STAGE;
+                    const uint32_t bar = mapa_shared(smem_u32(&full[s]), 0);
+                    if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * C::STAGE);
+                    tma_load_2d_pair(dst, &tmA, kb * fp8::BLOCK, tl.m0 + (int)rank * BM, bar);
+                    tma_load_3d_pair(dst + A_BYTES, &tmW, kb * fp8::BLOCK, tl.n0 + (int)rank * HN, tl.e, bar);
+                    ++issued;
+                }
+            }
+            ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+        }
+        // After a failed wait: both CTAs' copies count on the even CTA's barriers.
+        if (lane == 0 && !ok && rank == 0) {
+            for (uint32_t q = issued > STAGES ? issued - STAGES : 0; q < issued; ++q)
+                if (!mbar_wait_bounded(&full[q % STAGES], (q / STAGES) & 1)) break;
+        }
+        __syncwarp();
+    } else if (warp == WARP_MMA) {
+        if (rank == 0) {
+            for (int t = cid; ok && tiles.find(g, lane, t, tl); t += ncl) {
+                if (lane == 0) {
+                    for (int kb = 0; kb < nk; ++kb, ++it) {
+                        const uint32_t s = it % STAGES, b = it % NBUF;
+                        if ((it >= NBUF && !tc_wait(&tempty[b], ((it / NBUF) - 1) & 1, abort_flag)) ||
+                            !tc_wait(&full[s], (it / STAGES) & 1, abort_flag)) {
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after();
+                        const uint32_t a = smem_u32(ring + s * C::STAGE), w = a + A_BYTES;
+                        #pragma unroll
+                        for (int kk = 0; kk < 4; ++kk)
+                            mma_f8<2>(tmem_base + b * BN, umma_desc_sw128(a + kk * 32), umma_desc_sw128(w + kk * 32),
+                                      f8_idesc(2 * BM, BN), kk != 0 ? 1u : 0u);
+                        f4_commit<true>(&empty[s], 0x3);
+                        f4_commit<true>(&tfull[b], 0x3);
+                    }
+                }
+                ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+            }
+            if (lane == 0) {
+                f4_commit<true>(drain, 0x1);
+                mbar_wait_bounded(drain, 0);
+            }
+            __syncwarp();
+        }
+    } else {
+        const int quad = warp & 3, half = (warp - WARP_EPI0) >> 2;
+        uint8_t* stage = oring + (warp - WARP_EPI0) * OUT_BLOCK;
+        T* out = static_cast<T*>(g.out);
+        for (int t = cid; ok && tiles.find(g, lane, t, tl); t += ncl) {
+            const int mq = tl.m0 + (int)rank * BM + 32 * quad;       // first row of this warp
+            const int nh = tl.n0 + half * HN;                        // first column
+            // Rows past the group read the scale of its last row and are not stored.
+            const float* sa = g.sa + min(mq + lane, tl.r1 - 1);
+            const float* sw = g.sw + tl.e * g.sw_stride + min(nh, g.N - 1) / fp8::BLOCK;
+            auto scale = [&](int kb) { return kb < nk ? sa[kb * g.ldsa] * sw[kb * g.ldsw] : 0.0f; };
+            float2 acc[HN / 2];
+            #pragma unroll
+            for (int c = 0; c < HN / 2; ++c) acc[c] = make_float2(0.0f, 0.0f);
+            float s0 = scale(0), s1 = scale(1);
+            for (int kb = 0; kb < nk; ++kb, ++it) {
+                const uint32_t b = it % NBUF;
+                const float2 s = make_float2(s0, s0);
+                s0 = s1;
+                s1 = scale(kb + 2);
+                ok = __all_sync(0xffffffffu, tc_wait(&tfull[b], (it / NBUF) & 1, abort_flag));
+                if (!ok) break;
+                tc_fence_after();
+                const uint32_t t0 = tmem_base + ((uint32_t)(32 * quad) << 16) + b * BN + half * HN;
+                #pragma unroll
+                for (int c = 0; c < HN; c += 32) {
+                    uint32_t r[32];
+                    tmem_ld32_sync(t0 + c, r);
+                    if (c + 32 == HN) {
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) {
+                            if (rank == 0) mbar_arrive(&tempty[b]);
+                            else mbar_arrive_remote(&tempty[b], 0);
+                        }
+                    }
+                    #pragma unroll
+                    for (int j = 0; j < 32; j += 2)
+                        fma2(acc[(c + j) / 2], make_float2(__uint_as_float(r[j]), __uint_as_float(r[j + 1])), s);
+                }
+            }
+            if (!ok) break;
+            // 32 rows x 128 bytes at a time.
+            constexpr int PER = 128 / (int)sizeof(T);                // columns per pass
+            constexpr int CE = 16 / (int)sizeof(T);                  // elements per 16-byte chunk
+            #pragma unroll
+            for (int c = 0; c < HN; c += PER) {
+                #pragma unroll
+                for (int q = 0; q < 8; ++q) {
+                    uint4 v;
+                    T* e = reinterpret_cast<T*>(&v);
+                    #pragma unroll
+                    for (int i = 0; i < CE; ++i) {
+                        const int j = c + q * CE + i;
+                        e[i] = fp8_out<T>(j & 1 ? acc[j / 2].y : acc[j / 2].x);
+                    }
+                    *reinterpret_cast<uint4*>(stage + lane * 128 + ((q ^ (lane & 7)) << 4)) = v;
+                }
+                __syncwarp();
+                const int nb = nh + c;
+                if (vec_out) {
+                    #pragma unroll
+                    for (int p = 0; p < 8; ++p) {
+                        const int r = p * 4 + (lane >> 3), q = lane & 7, m = mq + r, n = nb + q * CE;
+                        const uint4 v = *reinterpret_cast<const uint4*>(stage + r * 128 + ((q ^ (r & 7)) << 4));
+                        if (m < tl.r1 && n < g.N) {
+                            T* dst = out + (int64_t)m * g.ldo + n;
+                            if (n + CE <= g.N) {
+                                *reinterpret_cast<uint4*>(dst) = v;
+                            } else {
+                                const T* e = reinterpret_cast<const T*>(&v);
+                                #pragma unroll
+                                for (int i = 0; i < CE; ++i)
+                                    if (n + i < g.N) dst[i] = e[i];
+                            }
+                        }
+                    }
+                } else {
+                    for (int r = 0; r < 32 && mq + r < tl.r1; ++r) {
+                        #pragma unroll
+                        for (int i = 0; i < PER; i += 32) {
+                            const int j = i + lane, n = nb + j;
+                            const T v = *reinterpret_cast<const T*>(stage + r * 128 + (((j / CE) ^ (r & 7)) << 4) +
+                                                                    (j % CE) * sizeof(T));
+                            if (n < g.N) out[(int64_t)(mq + r) * g.ldo + n] = v;
+                        }
+                    }
+                }
+                __syncwarp();
+            }
+        }
+    }
+    // The even CTA's MMAs read the odd one's shared and tensor memory.
+    tc_fence_before();
+    cluster_sync_all();
+    if (warp == WARP_MMA) {
+        tc_fence_after();
+        f4_tmem_dealloc<true>(tmem_base, 512);
     }
 }
 
