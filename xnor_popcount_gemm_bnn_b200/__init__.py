@@ -556,25 +556,44 @@ def bnn_binary_bases_gemm(H: torch.Tensor, J: int, B: torch.Tensor, I: int, K: i
 # 8-bit block-scaled products and the routing to experts
 # --------------------------------------------------------------------------
 
-_CODES = (torch.float8_e4m3fn, torch.uint8)
+_CODES = frozenset((torch.float8_e4m3fn, torch.uint8))
+_REAL = {torch.float32: BNN_F32, torch.bfloat16: BNN_BF16}
+_F32 = frozenset((torch.float32,))
+_I32 = frozenset((torch.int32,))
 
 
-def _same_device(*tensors: Optional[torch.Tensor]) -> None:
-    """Kernels launch on the current CUDA device: every tensor has to be there."""
-    d = torch.cuda.current_device()
-    for t in tensors:
-        if t is not None and (not t.is_cuda or t.get_device() != d):
-            raise ValueError(f"a tensor on {t.device}, with cuda:{d} as the current device")
+# The calls below are often shorter on the GPU than a Python call is long, so
+# their wrappers read each tensor's attributes once and pass plain integers.
+
+def _rows(t: torch.Tensor, dtypes, dev: int):
+    """(rows, columns, row stride) of a matrix of one of ``dtypes`` on device ``dev``, elements of a row adjacent; the
+    stride of a single row, which torch leaves arbitrary, is at least its width."""
+    rows, cols = t.shape
+    ld, unit = t.stride()
+    if t.dtype not in dtypes:
+        raise TypeError(f"unsupported dtype {t.dtype}")
+    if t.get_device() != dev:
+        raise ValueError(f"a tensor on {t.device}, with cuda:{dev} as the current device")
+    if unit != 1 and cols > 1:
+        raise ValueError("the elements of a row have to be adjacent")
+    return rows, cols, (ld if rows > 1 or ld > cols else cols)
 
 
-def _row_stride(t: torch.Tensor) -> int:
-    """Row stride of a matrix, at least its width (torch leaves the stride of a single row arbitrary)."""
-    return t.stride(-2) if t.shape[-2] > 1 else max(t.stride(-2), t.shape[-1])
+def _flat(t: torch.Tensor, n: int, dtypes, dev: int) -> int:
+    """Address of a contiguous tensor of n elements of one of ``dtypes`` on device ``dev``."""
+    if t.dtype not in dtypes:
+        raise TypeError(f"unsupported dtype {t.dtype}")
+    if t.get_device() != dev:
+        raise ValueError(f"a tensor on {t.device}, with cuda:{dev} as the current device")
+    if t.numel() != n or not t.is_contiguous():
+        raise ValueError(f"{n} contiguous elements are wanted, got {tuple(t.shape)} with strides {t.stride()}")
+    return t.data_ptr()
 
 
-def _unit(t: torch.Tensor) -> bool:
-    """Elements of a row next to each other (a single one has any stride)."""
-    return t.stride(-1) == 1 or t.shape[-1] <= 1
+def _raw_stream(stream, dev: int) -> int:
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(dev)
+    return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
 
 
 def bnn_fp8_ld_bytes(K: int) -> int:
@@ -585,61 +604,68 @@ def bnn_fp8_pack(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, blo
                  row_index: Optional[torch.Tensor] = None, K: Optional[int] = None, stream=None) -> None:
     """x [x_rows, K] (fp32/bf16, unit inner stride) -> e4m3 codes [rows, ld] (float8_e4m3fn or uint8) and block-major
     fp32 scales [ceil(K / 128), row blocks].  row_index int32 [rows]: the row of x of each packed row (block_rows 1)."""
-    _same_device(x, codes, scales, row_index)
-    x_rows, Kx = x.shape
-    rows = codes.shape[0]
+    dev = torch.cuda.current_device()
+    x_rows, Kx, ld_x = _rows(x, _REAL, dev)
+    rows, cols, ld_c = _rows(codes, _CODES, dev)
+    kb, nr, ld_s = _rows(scales, _F32, dev)
     K = Kx if K is None else int(K)
-    if not (_unit(x) and _unit(codes) and _unit(scales)) or codes.dtype not in _CODES or \
-            scales.dtype != torch.float32 or K > Kx or scales.shape[0] < (K + 127) // 128 or \
-            codes.shape[1] < bnn_fp8_ld_bytes(K) or scales.shape[1] < -(-rows // int(block_rows)):
-        raise ValueError("codes [rows, ld >= K rounded up to 16] and fp32 scales [blocks of K, row blocks], unit inner stride")
-    if row_index is not None and (row_index.dtype != torch.int32 or tuple(row_index.shape) != (rows,) or
-                                  not row_index.is_contiguous()):
-        raise ValueError("row_index is a contiguous int32 [rows]")
-    _check("bnn_fp8_pack", _lib.bnn_fp8_pack(
-        _ptr(x), _dtype(x), x_rows, K, _row_stride(x), _ptr(row_index), rows, int(block_rows), _ptr(codes),
-        _row_stride(codes), _ptr(scales), _row_stride(scales), _stream(stream)))
+    if K > Kx or kb * 128 < K or cols < (K + 15) // 16 * 16 or nr * block_rows < rows:
+        raise ValueError("sizes of codes [rows, K rounded up to 16] and scales [blocks of K, row blocks] do not fit")
+    index = None if row_index is None else _flat(row_index, rows, _I32, dev)
+    st = _lib.bnn_fp8_pack(x.data_ptr(), _REAL[x.dtype], x_rows, K, ld_x, index, rows, block_rows, codes.data_ptr(),
+                           ld_c, scales.data_ptr(), ld_s, _raw_stream(stream, dev))
+    if st:
+        _check("bnn_fp8_pack", st)
 
 
 def bnn_fp8_gemm(A: torch.Tensor, a_scales: torch.Tensor, W: torch.Tensor, w_scales: torch.Tensor, K: int,
                  out: torch.Tensor, stream=None) -> None:
     """out [M, N] (fp32/bf16) = A W^T for codes A [M, lda], W [N, ldw] with scales [ceil(K / 128), M] (one per row)
     and [ceil(K / 128), ceil(N / 128)] (one per 128 rows)."""
-    M, N, K = A.shape[0], W.shape[0], int(K)
-    _same_device(A, a_scales, W, w_scales, out)
-    _check_fp8(A, a_scales, W, w_scales, M, N, K, out)
-    _check("bnn_fp8_gemm", _lib.bnn_fp8_gemm(
-        _ptr(A), _row_stride(A), _ptr(a_scales), _row_stride(a_scales), _ptr(W), _row_stride(W), _ptr(w_scales),
-        _row_stride(w_scales), M, N, K, _ptr(out), _dtype(out), _row_stride(out), _stream(stream)))
+    dev = torch.cuda.current_device()
+    M, ka, lda = _rows(A, _CODES, dev)
+    N, kw, ldw = _rows(W, _CODES, dev)
+    ba, na, lsa = _rows(a_scales, _F32, dev)
+    bw, nw, lsw = _rows(w_scales, _F32, dev)
+    mo, no, ldo = _rows(out, _REAL, dev)
+    if ka < K or kw < K or ba * 128 < K or bw * 128 < K or na < M or nw * 128 < N or mo != M or no != N:
+        raise ValueError("sizes of codes, scales and out do not fit M, N and K")
+    st = _lib.bnn_fp8_gemm(A.data_ptr(), lda, a_scales.data_ptr(), lsa, W.data_ptr(), ldw, w_scales.data_ptr(), lsw,
+                           M, N, K, out.data_ptr(), _REAL[out.dtype], ldo, _raw_stream(stream, dev))
+    if st:
+        _check("bnn_fp8_gemm", st)
 
 
 def bnn_fp8_gemm_grouped(A: torch.Tensor, a_scales: torch.Tensor, offsets: torch.Tensor, W: torch.Tensor,
                          w_scales: torch.Tensor, K: int, out: torch.Tensor, stream=None) -> None:
     """Rows offsets[e] .. offsets[e + 1] of A [R, lda] times W[e]^T for W [E, N, ldw], w_scales
     [E, ceil(K / 128), ceil(N / 128)], offsets int32 [E + 1] on the device; out [R, N]."""
-    R, K = A.shape[0], int(K)
-    E, N = W.shape[:2]
-    _same_device(A, a_scales, offsets, W, w_scales, out)
-    if offsets.dtype != torch.int32 or tuple(offsets.shape) != (E + 1,) or not offsets.is_contiguous() or \
-            W.dim() != 3 or w_scales.dim() != 3 or w_scales.shape[0] != E:
-        raise ValueError("offsets int32 [E + 1], W [E, N, ld], w_scales [E, blocks of K, row blocks]")
-    _check_fp8(A, a_scales, W, w_scales, R, N, K, out)
-    _check("bnn_fp8_gemm_grouped", _lib.bnn_fp8_gemm_grouped(
-        _ptr(A), _row_stride(A), _ptr(a_scales), _row_stride(a_scales), R, _ptr(offsets), E, _ptr(W), _row_stride(W),
-        W.stride(0) if E > 1 else N * _row_stride(W), _ptr(w_scales), _row_stride(w_scales), w_scales.stride(0), N, K,
-        _ptr(out), _dtype(out), _row_stride(out), _stream(stream)))
-
-
-def _check_fp8(A, a_scales, W, w_scales, M, N, K, out) -> None:
-    kb, ld = (K + 127) // 128, (K + 15) // 16 * 16
-    if A.dtype not in _CODES or W.dtype not in _CODES or a_scales.dtype != torch.float32 or \
-            w_scales.dtype != torch.float32:
-        raise ValueError("codes are float8_e4m3fn or uint8, scales float32")
-    if A.shape[1] < ld or W.shape[-1] < ld or a_scales.shape[0] < kb or a_scales.shape[1] < M or \
-            w_scales.shape[-2] < kb or w_scales.shape[-1] < (N + 127) // 128 or tuple(out.shape) != (M, N):
-        raise ValueError("sizes of codes, scales and out do not fit M, N and K")
-    if not (_unit(A) and _unit(W) and _unit(a_scales) and _unit(w_scales) and _unit(out)):
-        raise ValueError("unit inner strides")
+    dev = torch.cuda.current_device()
+    R, ka, lda = _rows(A, _CODES, dev)
+    ba, na, lsa = _rows(a_scales, _F32, dev)
+    mo, no, ldo = _rows(out, _REAL, dev)
+    E, N, kw = W.shape
+    gw, ldw, uw = W.stride()
+    es, bw, nw = w_scales.shape
+    gs, lsw, us = w_scales.stride()
+    if W.dtype not in _CODES or w_scales.dtype is not torch.float32:
+        raise TypeError(f"unsupported dtypes {W.dtype}, {w_scales.dtype}")
+    if W.get_device() != dev or w_scales.get_device() != dev:
+        raise ValueError(f"tensors on {W.device} and {w_scales.device}, with cuda:{dev} as the current device")
+    if (uw != 1 and kw > 1) or (us != 1 and nw > 1):
+        raise ValueError("the elements of a row have to be adjacent")
+    if ka < K or kw < K or ba * 128 < K or bw * 128 < K or na < R or nw * 128 < N or mo != R or no != N or es != E:
+        raise ValueError("sizes of codes, scales and out do not fit R, E, N and K")
+    if N <= 1:
+        ldw = max(ldw, kw)
+    if bw <= 1:
+        lsw = max(lsw, nw)
+    st = _lib.bnn_fp8_gemm_grouped(
+        A.data_ptr(), lda, a_scales.data_ptr(), lsa, R, _flat(offsets, E + 1, _I32, dev), E, W.data_ptr(), ldw,
+        gw if E > 1 else N * ldw, w_scales.data_ptr(), lsw, gs, N, K, out.data_ptr(), _REAL[out.dtype], ldo,
+        _raw_stream(stream, dev))
+    if st:
+        _check("bnn_fp8_gemm_grouped", st)
 
 
 def bnn_route(logits: torch.Tensor, idx: torch.Tensor, weights: torch.Tensor, score: int = BNN_ROUTE_SOFTMAX,
@@ -648,38 +674,37 @@ def bnn_route(logits: torch.Tensor, idx: torch.Tensor, weights: torch.Tensor, sc
               row_token: Optional[torch.Tensor] = None, slot_row: Optional[torch.Tensor] = None, stream=None) -> None:
     """Choose k experts per token: logits [T, E] (fp32/bf16) -> idx int32 [T, k], weights fp32 [T, k]; with offsets
     int32 [E + 1], row_token int32 [T * k] and slot_row int32 [T, k] also the plan of rows by expert."""
-    T, E = logits.shape
-    k = idx.shape[1]
-    _same_device(logits, idx, weights, bias, offsets, row_token, slot_row)
-    if idx.dtype != torch.int32 or weights.dtype != torch.float32 or tuple(idx.shape) != (T, k) or \
-            tuple(weights.shape) != (T, k) or not idx.is_contiguous() or not weights.is_contiguous() or \
-            not _unit(logits):
-        raise ValueError("logits [T, E] of unit inner stride, idx int32 [T, k] and weights float32 [T, k], contiguous")
-    for t, n in ((offsets, E + 1), (row_token, T * k), (slot_row, T * k)):
-        if t is not None and (t.dtype != torch.int32 or t.numel() != n or not t.is_contiguous()):
-            raise ValueError("offsets int32 [E + 1], row_token int32 [T * k], slot_row int32 [T, k], contiguous")
-    if bias is not None and (bias.dtype != torch.float32 or tuple(bias.shape) != (E,) or not bias.is_contiguous()):
-        raise ValueError("bias is a contiguous float32 [E]")
-    p = bnn_route_params(int(score), k, int(n_groups), int(kept_groups), int(group_top), int(bool(renormalize)),
-                         float(scale), _ptr(bias))
-    _check("bnn_route", _lib.bnn_route(
-        _ptr(logits), _dtype(logits), T, E, _row_stride(logits), ctypes.byref(p), _ptr(idx), _ptr(weights),
-        _ptr(offsets), _ptr(row_token), _ptr(slot_row), _stream(stream)))
+    dev = torch.cuda.current_device()
+    T, E, ld = _rows(logits, _REAL, dev)
+    ti, k = idx.shape
+    n = T * k
+    if ti != T or tuple(weights.shape) != (T, k):
+        raise ValueError("idx and weights are [T, k]")
+    p = bnn_route_params(score, k, n_groups, kept_groups, group_top, 1 if renormalize else 0, scale,
+                         None if bias is None else _flat(bias, E, _F32, dev))
+    st = _lib.bnn_route(
+        logits.data_ptr(), _REAL[logits.dtype], T, E, ld, ctypes.byref(p), _flat(idx, n, _I32, dev),
+        _flat(weights, n, _F32, dev), None if offsets is None else _flat(offsets, E + 1, _I32, dev),
+        None if row_token is None else _flat(row_token, n, _I32, dev),
+        None if slot_row is None else _flat(slot_row, n, _I32, dev), _raw_stream(stream, dev))
+    if st:
+        _check("bnn_route", st)
 
 
 def bnn_route_combine(Y: torch.Tensor, slot_row: torch.Tensor, weights: torch.Tensor, out: torch.Tensor,
                       stream=None) -> None:
     """out [T, N] = sum over j of weights[t, j] * Y[slot_row[t, j]] (Y [R, N], fp32/bf16)."""
+    dev = torch.cuda.current_device()
+    R, N, ldy = _rows(Y, _REAL, dev)
+    to, no, ldo = _rows(out, _REAL, dev)
     T, k = weights.shape
-    R, N = Y.shape
-    _same_device(Y, slot_row, weights, out)
-    if slot_row.dtype != torch.int32 or weights.dtype != torch.float32 or slot_row.numel() != T * k or \
-            not slot_row.is_contiguous() or not weights.is_contiguous() or tuple(out.shape) != (T, N) or \
-            not (_unit(Y) and _unit(out)):
-        raise ValueError("slot_row int32 [T, k] and weights float32 [T, k], contiguous; Y [R, N], out [T, N]")
-    _check("bnn_route_combine", _lib.bnn_route_combine(
-        _ptr(Y), _dtype(Y), R, N, _row_stride(Y), _ptr(slot_row), _ptr(weights), T, k, _ptr(out), _dtype(out),
-        _row_stride(out), _stream(stream)))
+    if to != T or no != N:
+        raise ValueError("out is [T, N]")
+    st = _lib.bnn_route_combine(Y.data_ptr(), _REAL[Y.dtype], R, N, ldy, _flat(slot_row, T * k, _I32, dev),
+                                _flat(weights, T * k, _F32, dev), T, k, out.data_ptr(), _REAL[out.dtype], ldo,
+                                _raw_stream(stream, dev))
+    if st:
+        _check("bnn_route_combine", st)
 
 
 def empty_fp8(rows: int, K: int, device="cuda") -> torch.Tensor:
