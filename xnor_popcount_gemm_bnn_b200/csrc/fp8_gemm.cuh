@@ -76,6 +76,58 @@ __host__ __device__ constexpr uint32_t f8_idesc(int m, int n) {
     return (1u << 4) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
 }
 
+// tc_wait for waits that come once per K block: the timer is read only after
+// the wait has failed for a while.
+__device__ __forceinline__ bool f8_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
+    #pragma unroll 1
+    for (int i = 0; i < 64; ++i)
+        if (mbar_try_wait(bar, parity)) return true;
+    return tc_wait(bar, parity, abort_flag);
+}
+// True in one lane of a converged warp.  The compiler knows that one lane
+// runs what this guards, and issues tensor-core and copy instructions there
+// without a loop over the lanes.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(p));
+    return p != 0;
+}
+// f8_wait by one lane for its warp.
+__device__ __forceinline__ bool f8_wait_warp(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int lane) {
+    int ok = 1;
+    if (lane == 0) ok = f8_wait(bar, parity, abort_flag) ? 1 : 0;
+    return __shfl_sync(0xffffffffu, ok, 0) != 0;
+}
+
+__device__ __forceinline__ void cp_async4(void* dst, const void* src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// f8_wait by all lanes of a converged warp, which stay converged.
+__device__ __forceinline__ bool f8_wait_all(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
+    #pragma unroll 1
+    for (int i = 0; i < 64; ++i)
+        if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+    return __all_sync(0xffffffffu, tc_wait(bar, parity, abort_flag));
+}
+
+// Arrive on an mbarrier given by its address in the cluster's shared memory,
+// without ordering earlier memory operations (a release over the cluster costs
+// about a thousand cycles here): for an arrival that only says that values
+// have come into registers.
+__device__ __forceinline__ void mbar_arrive_relaxed(uint32_t addr) {
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
+}
+
 // acc += t * s on pairs of fp32 (one instruction per two products).
 __device__ __forceinline__ void fma2(float2& acc, float2 t, float2 s) {
     asm("fma.rn.f32x2 %0, %1, %2, %0;"
@@ -193,41 +245,39 @@ fp8_gemm_split_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_cons
     bool ok = true;
     for (int m0 = rows.x + (int)blockIdx.y * NT; m0 < rows.y; m0 += (int)gridDim.y * NT) {
         if (warp == WARP_PRODUCER) {
-            if (lane == 0) {
-                for (int kb = kb0; ok && kb < kb1; ++kb, ++it) {
-                    const uint32_t s = it % STAGES;
-                    if (it >= STAGES && !tc_wait(&empty[s], ((it / STAGES) - 1) & 1, abort_flag)) {
-                        ok = false;
-                        break;
-                    }
+            for (int kb = kb0; ok && kb < kb1; ++kb, ++it) {
+                const uint32_t s = it % STAGES;
+                ok = it < STAGES || f8_wait_warp(&empty[s], ((it / STAGES) - 1) & 1, abort_flag, lane);
+                if (!ok) break;
+                if (elect_one()) {
                     uint8_t* dst = ring + s * C::STAGE;
                     mbar_arrive_expect_tx(&full[s], C::STAGE);
                     tma_load_3d(dst, &tmW, kb * fp8::BLOCK, n0, e, &full[s]);
                     tma_load_2d(dst + W_BYTES, &tmA, kb * fp8::BLOCK, m0, &full[s]);
-                    ++issued;
                 }
+                __syncwarp();
+                ++issued;
             }
-            __syncwarp();
         } else if (warp == WARP_MMA) {
-            if (lane == 0) {
-                for (int kb = kb0; ok && kb < kb1; ++kb, ++it) {
-                    const uint32_t s = it % STAGES, b = it % NBUF;
-                    if ((it >= NBUF && !tc_wait(&tempty[b], ((it / NBUF) - 1) & 1, abort_flag)) ||
-                        !tc_wait(&full[s], (it / STAGES) & 1, abort_flag)) {
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
-                    const uint32_t w = smem_u32(ring + s * C::STAGE), a = w + W_BYTES;
+            // Stages lie 16-byte units apart in the descriptor's address field
+            // (a shared-memory address never carries out of it).
+            const uint64_t wdesc = umma_desc_sw128(smem_u32(ring));
+            for (int kb = kb0; ok && kb < kb1; ++kb, ++it) {
+                const uint32_t s = it % STAGES, b = it % NBUF;
+                ok = (it < NBUF || f8_wait_warp(&tempty[b], ((it / NBUF) - 1) & 1, abort_flag, lane)) &&
+                     f8_wait_warp(&full[s], (it / STAGES) & 1, abort_flag, lane);
+                if (!ok) break;
+                tc_fence_after();
+                if (elect_one()) {
+                    const uint64_t dw = wdesc + (uint64_t)(s * (C::STAGE >> 4)), da = dw + (W_BYTES >> 4);
                     #pragma unroll
                     for (int kk = 0; kk < 4; ++kk)
-                        mma_f8<1>(tmem_base + b * NT, umma_desc_sw128(w + kk * 32), umma_desc_sw128(a + kk * 32),
-                                  f8_idesc(BN, NT), kk != 0 ? 1u : 0u);
+                        mma_f8<1>(tmem_base + b * NT, dw + kk * 2, da + kk * 2, f8_idesc(BN, NT), kk != 0 ? 1u : 0u);
                     mma_commit(&empty[s]);
                     mma_commit(&tfull[b]);
                 }
+                __syncwarp();
             }
-            __syncwarp();
         } else {
             const int quad = warp & 3, tid = (int)threadIdx.x - WARP_EPI0 * 32;
             const int cols = min(NT, rows.y - m0);
@@ -244,7 +294,7 @@ fp8_gemm_split_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_cons
             for (int kb = kb0; kb < kb1; ++kb, ++it) {
                 const uint32_t b = it % NBUF;
                 const float* s = sbuf + ((kb - kb0) & 1) * NT;
-                ok = ok && __all_sync(0xffffffffu, tc_wait(&tfull[b], (it / NBUF) & 1, abort_flag));
+                ok = ok && f8_wait_warp(&tfull[b], (it / NBUF) & 1, abort_flag, lane);
                 if (ok) {
                     tc_fence_after();
                     const uint32_t t0 = tmem_base + ((uint32_t)(32 * quad) << 16) + b * NT;
@@ -317,7 +367,7 @@ fp8_gemm_split_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_cons
         for (uint32_t q = issued > STAGES ? issued - STAGES : 0; q < issued; ++q)
             if (!mbar_wait_bounded(&full[q % STAGES], (q / STAGES) & 1)) break;
     }
-    if (warp == WARP_MMA && lane == 0) {
+    if (warp == WARP_MMA && elect_one()) {
         mma_commit(drain);
         mbar_wait_bounded(drain, 0);
     }
@@ -336,18 +386,23 @@ fp8_gemm_split_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_cons
 namespace f8p {
 constexpr int BM = 128;                      // rows of A per CTA = TMEM lanes
 constexpr int A_BYTES = BM * fp8::BLOCK;     // 16 KiB per stage
-constexpr int WARP_PRODUCER = 0, WARP_MMA = 1, WARP_EPI0 = 2, EPI_WARPS = 8;
+constexpr int WARP_PRODUCER = 0, WARP_MMA = 1, WARP_SCALE = 2, WARP_EPI0 = 4, EPI_WARPS = 16;
 constexpr int THREADS = (WARP_EPI0 + EPI_WARPS) * 32;
-constexpr int OUT_BLOCK = 32 * 128;          // staging per epilogue warp: 32 rows x 128 bytes
+constexpr int AHEAD = 4;                     // K blocks whose scales are in flight
+constexpr int OUT_ROW = 64;                  // bytes per row of an epilogue warp's staging block
+constexpr int OUT_BLOCK = 32 * OUT_ROW;
 constexpr int BAND = 8;                      // row tiles that a band of concurrent tiles spans
 template <int BN>
 struct Cfg {
     static constexpr int W_BYTES = BN / 2 * fp8::BLOCK;      // this CTA's half of the weight rows
     static constexpr int STAGE = A_BYTES + W_BYTES;
-    static constexpr int FIXED = EPI_WARPS * OUT_BLOCK + 512 + 1024;
+    static constexpr int NBUF = 512 / BN;                    // accumulators in tensor memory
+    static constexpr int NBK = BN / fp8::BLOCK;              // column blocks of a tile
+    static constexpr int RAW_BYTES = AHEAD * (4 + NBK) * 32 * 4;
+    static constexpr int PROD_BYTES = 2 * NBUF * NBK * BM * 4;
+    static constexpr int FIXED = EPI_WARPS * OUT_BLOCK + RAW_BYTES + PROD_BYTES + 512 + 1024;
     static constexpr int STAGES = (tc::SMEM_LIMIT - FIXED) / STAGE;
     static constexpr int SMEM_BYTES = FIXED + STAGES * STAGE;
-    static constexpr int NBUF = 512 / BN;                    // accumulators in tensor memory
     static_assert((2 * STAGES + 2 * NBUF + 1) * 8 + 16 <= 512, "barriers");
     static_assert(STAGE % 1024 == 0, "128B swizzle");
 };
@@ -429,28 +484,36 @@ struct Fp8Tiles {
 // Persistent pairs of CTAs (cta_group::2), one CTA per SM:
 //  warp 0     producer in each CTA: its 128 rows of A and its half of the BN
 //             weight rows per K block, counted on the even CTA's barrier.
-//  warp 1     in the even CTA one thread issues the four MMAs of a K block
-//             (M = 256, N = BN) for both.
-//  warps 2-9  epilogue: warp quadrants of 32 rows, two warps per quadrant with
-//             half of the columns each; thread = one row, BN / 2 fp32 sums in
-//             registers, C += (sA[b, row] * sW[b, column block]) * inner.  Half
-//             a tile lies in one column block, so the factor is one number per
-//             thread and block, loaded two blocks ahead.
+//  warp 1     in the even CTA issues the four MMAs of a K block (M = 256,
+//             N = BN) for both.
+//  warp 2     scales: per K block sA[b, row] * sW[b, column block] for the
+//             CTA's rows and the tile's column blocks, copied AHEAD blocks
+//             ahead and put into shared memory; its arrival on the
+//             accumulator's barrier goes with the MMAs' commit.
+//  warps 4-19 epilogue: four warps per quadrant of 32 rows, a quarter of the
+//             columns each; thread = one row, BN / 4 fp32 sums in registers,
+//             C += scale * inner, one scale per thread and block.
 // The tensor memory holds 512 / BN accumulators: the MMAs of the next blocks
-// run while the epilogue adds this one.  The finished tile is rounded, put
-// into shared memory (16-byte chunks swizzled by row, no bank conflicts) and
-// stored in whole 128-byte lines by row, rows and columns outside left out.
+// run while the epilogue adds this one.  What bounds the kernel is the
+// epilogue's latency per block (wait, tensor-memory load, multiply-add, hand
+// back), which is why its loop holds nothing else and four warps per scheduler
+// take turns.  The finished tile is rounded, put into shared memory (16-byte
+// chunks swizzled by row, no bank conflicts) and stored by row, rows and
+// columns outside left out.
 template <int BN, typename T>
 __global__ void __launch_bounds__(f8p::THREADS, 1)
 fp8_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmW, Fp8Gemm g,
                      int vec_out) {
     using namespace f8p;
     using C = Cfg<BN>;
-    constexpr int STAGES = C::STAGES, NBUF = C::NBUF, HN = BN / 2;
+    constexpr int STAGES = C::STAGES, NBUF = C::NBUF, NBK = C::NBK;
+    constexpr int CW = BN / (EPI_WARPS / 4);                               // columns of an epilogue warp
     extern __shared__ uint8_t smem_raw[];
     uint8_t* ring = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     uint8_t* oring = ring + STAGES * C::STAGE;
-    uint64_t* full = reinterpret_cast<uint64_t*>(oring + EPI_WARPS * OUT_BLOCK);
+    float* raw = reinterpret_cast<float*>(oring + EPI_WARPS * OUT_BLOCK);  // [AHEAD][4 + NBK][32]
+    float* prod = raw + C::RAW_BYTES / 4;                                  // [2 NBUF][NBK][BM]
+    uint64_t* full = reinterpret_cast<uint64_t*>(prod + C::PROD_BYTES / 4);
     uint64_t* empty = full + STAGES;
     uint64_t* tfull = empty + STAGES;
     uint64_t* tempty = tfull + NBUF;
@@ -471,7 +534,7 @@ fp8_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
             mbar_init(&empty[s], 1);
         }
         for (int b = 0; b < NBUF; ++b) {
-            mbar_init(&tfull[b], 1);
+            mbar_init(&tfull[b], 2);                   // the MMAs' commit and the scales
             mbar_init(&tempty[b], EPI_WARPS * 2);
         }
         mbar_init(drain, 1);
@@ -494,22 +557,20 @@ fp8_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
     if (warp == WARP_PRODUCER) {
         uint32_t issued = 0;
         for (int t = cid; ok && tiles.find(g, lane, t, tl); t += ncl) {
-            if (lane == 0) {
-                for (int kb = 0; kb < nk; ++kb, ++it) {
-                    const uint32_t s = it % STAGES;
-                    if (it >= STAGES && !tc_wait(&empty[s], ((it / STAGES) - 1) & 1, abort_flag)) {
-                        ok = false;
-                        break;
-                    }
+            for (int kb = 0; kb < nk; ++kb, ++it) {
+                const uint32_t s = it % STAGES;
+                ok = it < STAGES || f8_wait_warp(&empty[s], ((it / STAGES) - 1) & 1, abort_flag, lane);
+                if (!ok) break;
+                if (elect_one()) {
                     uint8_t* dst = ring + s * C::STAGE;
                     const uint32_t bar = mapa_shared(smem_u32(&full[s]), 0);
                     if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * C::STAGE);
                     tma_load_2d_pair(dst, &tmA, kb * fp8::BLOCK, tl.m0 + (int)rank * BM, bar);
-                    tma_load_3d_pair(dst + A_BYTES, &tmW, kb * fp8::BLOCK, tl.n0 + (int)rank * HN, tl.e, bar);
-                    ++issued;
+                    tma_load_3d_pair(dst + A_BYTES, &tmW, kb * fp8::BLOCK, tl.n0 + (int)rank * (BN / 2), tl.e, bar);
                 }
+                __syncwarp();
+                ++issued;
             }
-            ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
         }
         // After a failed wait: both CTAs' copies count on the even CTA's barriers.
         if (lane == 0 && !ok && rank == 0) {
@@ -519,82 +580,122 @@ fp8_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
         __syncwarp();
     } else if (warp == WARP_MMA) {
         if (rank == 0) {
+            // Stages lie 16-byte units apart in the descriptor's address field
+            // (a shared-memory address never carries out of it).
+            const uint64_t adesc = umma_desc_sw128(smem_u32(ring));
             for (int t = cid; ok && tiles.find(g, lane, t, tl); t += ncl) {
-                if (lane == 0) {
-                    for (int kb = 0; kb < nk; ++kb, ++it) {
-                        const uint32_t s = it % STAGES, b = it % NBUF;
-                        if ((it >= NBUF && !tc_wait(&tempty[b], ((it / NBUF) - 1) & 1, abort_flag)) ||
-                            !tc_wait(&full[s], (it / STAGES) & 1, abort_flag)) {
-                            ok = false;
-                            break;
-                        }
-                        tc_fence_after();
-                        const uint32_t a = smem_u32(ring + s * C::STAGE), w = a + A_BYTES;
+                for (int kb = 0; kb < nk; ++kb, ++it) {
+                    const uint32_t s = it % STAGES, b = it % NBUF;
+                    const uint64_t da = adesc + (uint64_t)(s * (C::STAGE >> 4)), dw = da + (A_BYTES >> 4);
+                    ok = f8_wait_all(&full[s], (it / STAGES) & 1, abort_flag) &&
+                         (it < NBUF || f8_wait_all(&tempty[b], ((it / NBUF) - 1) & 1, abort_flag));
+                    if (!ok) break;
+                    tc_fence_after();
+                    if (elect_one()) {
                         #pragma unroll
                         for (int kk = 0; kk < 4; ++kk)
-                            mma_f8<2>(tmem_base + b * BN, umma_desc_sw128(a + kk * 32), umma_desc_sw128(w + kk * 32),
-                                      f8_idesc(2 * BM, BN), kk != 0 ? 1u : 0u);
-                        f4_commit<true>(&empty[s], 0x3);
+                            mma_f8<2>(tmem_base + b * BN, da + kk * 2, dw + kk * 2, f8_idesc(2 * BM, BN),
+                                      kk != 0 ? 1u : 0u);
                         f4_commit<true>(&tfull[b], 0x3);
+                        f4_commit<true>(&empty[s], 0x3);
                     }
+                    __syncwarp();
                 }
-                ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
             }
-            if (lane == 0) {
+            if (elect_one()) {
                 f4_commit<true>(drain, 0x1);
                 mbar_wait_bounded(drain, 0);
             }
             __syncwarp();
         }
-    } else {
-        const int quad = warp & 3, half = (warp - WARP_EPI0) >> 2;
+    } else if (warp == WARP_SCALE) {
+        for (int t = cid; ok && tiles.find(g, lane, t, tl); t += ncl) {
+            // Rows and columns past the ends take the last one's scale; they are not stored.
+            const float* sa[4];
+            const float* sw[NBK];
+            #pragma unroll
+            for (int i = 0; i < 4; ++i) sa[i] = g.sa + min(tl.m0 + (int)rank * BM + 32 * i + lane, tl.r1 - 1);
+            #pragma unroll
+            for (int i = 0; i < NBK; ++i)
+                sw[i] = g.sw + tl.e * g.sw_stride + min(tl.n0 + i * fp8::BLOCK, g.N - 1) / fp8::BLOCK;
+            // Every lane copies what it needs itself, so only its own copies are waited for.
+            auto load = [&](int kb) {
+                if (kb < nk) {
+                    float* d = raw + (kb % AHEAD) * (4 + NBK) * 32 + lane;
+                    #pragma unroll
+                    for (int i = 0; i < 4; ++i) cp_async4(d + 32 * i, sa[i] + kb * g.ldsa);
+                    #pragma unroll
+                    for (int i = 0; i < NBK; ++i) cp_async4(d + 32 * (4 + i), sw[i] + kb * g.ldsw);
+                }
+                cp_async_commit();
+            };
+            #pragma unroll
+            for (int i = 0; i < AHEAD - 1; ++i) load(i);
+            for (int kb = 0; kb < nk; ++kb, ++it) {
+                const uint32_t b = it % NBUF;
+                load(kb + AHEAD - 1);
+                cp_async_wait<AHEAD - 1>();
+                // The accumulator's previous use is committed: its barrier can
+                // take this block's arrival, and the epilogue is done with the
+                // block 2 NBUF before this one (the MMAs had waited for it).
+                ok = it < NBUF || f8_wait_all(&tfull[b], ((it / NBUF) - 1) & 1, abort_flag);
+                if (!ok) break;
+                const float* d = raw + (kb % AHEAD) * (4 + NBK) * 32 + lane;
+                float* p = prod + (it % (2 * NBUF)) * NBK * BM + lane;
+                #pragma unroll
+                for (int n = 0; n < NBK; ++n) {
+                    const float w = d[32 * (4 + n)];
+                    #pragma unroll
+                    for (int i = 0; i < 4; ++i) p[n * BM + 32 * i] = d[32 * i] * w;
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&tfull[b]);
+            }
+        }
+    } else if (warp >= WARP_EPI0) {
+        const int quad = warp & 3, part = (warp - WARP_EPI0) >> 2;
         uint8_t* stage = oring + (warp - WARP_EPI0) * OUT_BLOCK;
+        const uint32_t hand_back = mapa_shared(smem_u32(tempty), 0);
+        const float* sp = prod + part * CW / fp8::BLOCK * BM + 32 * quad + lane;
+        const uint32_t tq = tmem_base + ((uint32_t)(32 * quad) << 16) + part * CW;
         T* out = static_cast<T*>(g.out);
         for (int t = cid; ok && tiles.find(g, lane, t, tl); t += ncl) {
             const int mq = tl.m0 + (int)rank * BM + 32 * quad;       // first row of this warp
-            const int nh = tl.n0 + half * HN;                        // first column
-            // Rows past the group read the scale of its last row and are not stored.
-            const float* sa = g.sa + min(mq + lane, tl.r1 - 1);
-            const float* sw = g.sw + tl.e * g.sw_stride + min(nh, g.N - 1) / fp8::BLOCK;
-            auto scale = [&](int kb) { return kb < nk ? sa[kb * g.ldsa] * sw[kb * g.ldsw] : 0.0f; };
-            float2 acc[HN / 2];
+            const int nh = tl.n0 + part * CW;                        // first column
+            float2 acc[CW / 2];
             #pragma unroll
-            for (int c = 0; c < HN / 2; ++c) acc[c] = make_float2(0.0f, 0.0f);
-            float s0 = scale(0), s1 = scale(1);
+            for (int c = 0; c < CW / 2; ++c) acc[c] = make_float2(0.0f, 0.0f);
+            #pragma unroll 1
             for (int kb = 0; kb < nk; ++kb, ++it) {
                 const uint32_t b = it % NBUF;
-                const float2 s = make_float2(s0, s0);
-                s0 = s1;
-                s1 = scale(kb + 2);
-                ok = __all_sync(0xffffffffu, tc_wait(&tfull[b], (it / NBUF) & 1, abort_flag));
+                ok = f8_wait_all(&tfull[b], (it / NBUF) & 1, abort_flag);
                 if (!ok) break;
                 tc_fence_after();
-                const uint32_t t0 = tmem_base + ((uint32_t)(32 * quad) << 16) + b * BN + half * HN;
+                const float f = sp[(it % (2 * NBUF)) * NBK * BM];
+                const float2 s = make_float2(f, f);
                 #pragma unroll
-                for (int c = 0; c < HN; c += 32) {
-                    uint32_t r[32];
-                    tmem_ld32_sync(t0 + c, r);
-                    if (c + 32 == HN) {
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) {
-                            if (rank == 0) mbar_arrive(&tempty[b]);
-                            else mbar_arrive_remote(&tempty[b], 0);
-                        }
-                    }
+                for (int c = 0; c < CW; c += 16) {
+                    uint32_t r[16];
+                    tmem_ld16_sync(tq + b * BN + c, r);
                     #pragma unroll
-                    for (int j = 0; j < 32; j += 2)
+                    for (int j = 0; j < 16; j += 2)
                         fma2(acc[(c + j) / 2], make_float2(__uint_as_float(r[j]), __uint_as_float(r[j + 1])), s);
                 }
+                tc_fence_before();
+                // The loads have completed (wait::ld) and the scale was used: nothing
+                // of this block is read after the arrival.
+                if (elect_one()) mbar_arrive_relaxed(hand_back + b * 8);
             }
             if (!ok) break;
-            // 32 rows x 128 bytes at a time.
-            constexpr int PER = 128 / (int)sizeof(T);                // columns per pass
+            // 32 rows x 64 bytes at a time: chunk q of row r at (q ^ (r >> 1 & 3)) * 16.
             constexpr int CE = 16 / (int)sizeof(T);                  // elements per 16-byte chunk
+            constexpr int CQ = OUT_ROW / 16;                         // chunks per row and pass
+            constexpr int PER = CQ * CE;                             // columns per pass
+            static_assert(CW % PER == 0, "whole passes");
             #pragma unroll
-            for (int c = 0; c < HN; c += PER) {
+            for (int c = 0; c < CW; c += PER) {
                 #pragma unroll
-                for (int q = 0; q < 8; ++q) {
+                for (int q = 0; q < CQ; ++q) {
                     uint4 v;
                     T* e = reinterpret_cast<T*>(&v);
                     #pragma unroll
@@ -602,15 +703,15 @@ fp8_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
                         const int j = c + q * CE + i;
                         e[i] = fp8_out<T>(j & 1 ? acc[j / 2].y : acc[j / 2].x);
                     }
-                    *reinterpret_cast<uint4*>(stage + lane * 128 + ((q ^ (lane & 7)) << 4)) = v;
+                    *reinterpret_cast<uint4*>(stage + lane * OUT_ROW + ((q ^ ((lane >> 1) & 3)) << 4)) = v;
                 }
                 __syncwarp();
                 const int nb = nh + c;
                 if (vec_out) {
                     #pragma unroll
-                    for (int p = 0; p < 8; ++p) {
-                        const int r = p * 4 + (lane >> 3), q = lane & 7, m = mq + r, n = nb + q * CE;
-                        const uint4 v = *reinterpret_cast<const uint4*>(stage + r * 128 + ((q ^ (r & 7)) << 4));
+                    for (int p = 0; p < CQ; ++p) {
+                        const int r = p * (32 / CQ) + lane / CQ, q = lane % CQ, m = mq + r, n = nb + q * CE;
+                        const uint4 v = *reinterpret_cast<const uint4*>(stage + r * OUT_ROW + ((q ^ ((r >> 1) & 3)) << 4));
                         if (m < tl.r1 && n < g.N) {
                             T* dst = out + (int64_t)m * g.ldo + n;
                             if (n + CE <= g.N) {
@@ -624,14 +725,12 @@ fp8_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
                         }
                     }
                 } else {
-                    for (int r = 0; r < 32 && mq + r < tl.r1; ++r) {
-                        #pragma unroll
-                        for (int i = 0; i < PER; i += 32) {
-                            const int j = i + lane, n = nb + j;
-                            const T v = *reinterpret_cast<const T*>(stage + r * 128 + (((j / CE) ^ (r & 7)) << 4) +
-                                                                    (j % CE) * sizeof(T));
-                            if (n < g.N) out[(int64_t)(mq + r) * g.ldo + n] = v;
-                        }
+                    // Any alignment: elements one by one, a row's next to each other.
+                    for (int i = lane; i < 32 * PER; i += 32) {
+                        const int r = i / PER, j = i % PER, m = mq + r, n = nb + j;
+                        const T v = *reinterpret_cast<const T*>(stage + r * OUT_ROW +
+                                                                (((j / CE) ^ ((r >> 1) & 3)) << 4) + (j % CE) * sizeof(T));
+                        if (m < tl.r1 && n < g.N) out[(int64_t)m * g.ldo + n] = v;
                     }
                 }
                 __syncwarp();
