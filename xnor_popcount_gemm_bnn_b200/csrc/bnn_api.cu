@@ -1747,12 +1747,12 @@ bool encode_fp8_map(CUtensorMap* map, const uint8_t* base, int64_t K, int64_t ro
 
 // Per-device one-time opt-in of the 8-bit kernels to their shared memory; the
 // number of CTA pairs that fit on the device at once, or -1.
-template <int NT>
+template <int NT, bool DEEP>
 bool fp8_split_opt_in() {
-    constexpr int bytes = bnn::f8s::Cfg<NT>::SMEM_BYTES;
-    return cudaFuncSetAttribute(bnn::fp8_gemm_split_kernel<NT, float>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                bytes) == cudaSuccess &&
-           cudaFuncSetAttribute(bnn::fp8_gemm_split_kernel<NT, __nv_bfloat16>,
+    constexpr int bytes = bnn::f8s::Cfg<NT, DEEP>::SMEM_BYTES;
+    return cudaFuncSetAttribute(bnn::fp8_gemm_split_kernel<NT, DEEP, float>,
+                                cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) == cudaSuccess &&
+           cudaFuncSetAttribute(bnn::fp8_gemm_split_kernel<NT, DEEP, __nv_bfloat16>,
                                 cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) == cudaSuccess;
 }
 template <int BN>
@@ -1772,7 +1772,8 @@ int fp8_pairs_resident() {
         const int p = pairs[dev].load(std::memory_order_acquire);
         if (p > 0) return p;
     }
-    if (!fp8_split_opt_in<16>() || !fp8_split_opt_in<32>() || !fp8_split_opt_in<64>() || !fp8_split_opt_in<128>() ||
+    if (!fp8_split_opt_in<16, false>() || !fp8_split_opt_in<16, true>() || !fp8_split_opt_in<32, true>() ||
+        !fp8_split_opt_in<64, true>() || !fp8_split_opt_in<128, true>() ||
         !fp8_pair_opt_in<128>() || !fp8_pair_opt_in<256>())
         return -1;
     cudaLaunchConfig_t cfg = {};
@@ -1826,30 +1827,50 @@ struct Fp8Operands {
     int64_t lda, ldw, w_stride;
 };
 
+// Split of K for `tiles` clusters: as many CTAs as the SMs hold at once
+// (`slots`), at the fewest K blocks that a CTA takes one after the other, plus
+// about four blocks' time to start and to add the parts.  Up to two rounds a
+// begun one counts whole; later ones overlap.
+int fp8_split(int64_t tiles, int64_t slots, int64_t nk) {
+    int best = 1;
+    double best_cost = 1e300;
+    for (int s = 1; s <= bnn::f8s::MAX_SPLIT && s <= nk; ++s) {
+        const double rounds = (double)(tiles * s) / (double)slots;
+        const double cost = (rounds <= 2.0 ? std::ceil(rounds) : rounds + 0.5) * (double)(ceil_div(nk, s) + 4);
+        if (cost < best_cost) {
+            best_cost = cost;
+            best = s;
+        }
+    }
+    return best;
+}
+
+template <int NT, bool DEEP, typename T>
+bnn_status launch_fp8_split_as(const CUtensorMap& tmA, const CUtensorMap& tmW, const bnn::Fp8Gemm& g, int64_t chunks,
+                               int64_t tiles_n, int S, cudaStream_t stream) {
+    using C = bnn::f8s::Cfg<NT, DEEP>;
+    const int vec = aligned(g.out, 4 * sizeof(T)) && g.ldo % 4 == 0 ? 1 : 0;
+    return launch_clusters(bnn::fp8_gemm_split_kernel<NT, DEEP, T>,
+                           dim3((unsigned)(tiles_n * g.E * S), (unsigned)chunks), C::THREADS, C::SMEM_BYTES, S, stream,
+                           tmA, tmW, g, (int)tiles_n, S, vec);
+}
+
 template <int NT, typename T>
 bnn_status launch_fp8_split(const Fp8Operands& o, const bnn::Fp8Gemm& g, int64_t chunks, cudaStream_t stream) {
-    using C = bnn::f8s::Cfg<NT>;
     CUtensorMap tmA, tmW;
     if (!encode_fp8_map(&tmA, o.A, g.K, g.R, o.lda, 0, 0, NT) ||
         !encode_fp8_map(&tmW, o.W, g.K, g.N, o.ldw, g.E, o.w_stride, bnn::f8s::BN))
         return BNN_ERR_CUDA;
-    const int64_t tiles_n = ceil_div(g.N, bnn::f8s::BN), tiles = tiles_n * g.E;
-    const int64_t nk = ceil_div(g.K, bnn::fp8::BLOCK);
-    // Split of K: as many CTAs as fill the SMs twice, at the fewest K blocks a
-    // CTA has to take one after the other (plus about four blocks' time to
-    // start and to add the parts).
-    const int64_t slots = 2 * (int64_t)sm_count();
-    int S = 1;
-    int64_t best = INT64_MAX;
-    for (int s = 1; s <= bnn::f8s::MAX_SPLIT && s <= nk; ++s) {
-        const int64_t cost = ceil_div(tiles * chunks * s, slots) * (ceil_div(nk, s) + 4);
-        if (cost < best) {
-            best = cost;
-            S = s;
-        }
+    const int64_t tiles_n = ceil_div(g.N, bnn::f8s::BN), nk = ceil_div(g.K, bnn::fp8::BLOCK);
+    const int S = fp8_split(tiles_n * g.E * chunks, (int64_t)bnn::f8s::Cfg<NT, true>::PER_SM * sm_count(), nk);
+    if constexpr (NT == 16) {
+        // A short stream per CTA is bound by the launch: the shallow ring
+        // lets the next launch set up beside it (11008 x 4096, 11 blocks per
+        // CTA: 10.7 us against 11.5).  A long one by memory: the deep ring (64
+        // experts of 2048 x 4096, 32 blocks: 68 us against 82).
+        if (ceil_div(nk, S) <= 16) return launch_fp8_split_as<NT, false, T>(tmA, tmW, g, chunks, tiles_n, S, stream);
     }
-    return launch_clusters(bnn::fp8_gemm_split_kernel<NT, T>, dim3((unsigned)(tiles * S), (unsigned)chunks),
-                           bnn::f8s::THREADS, C::SMEM_BYTES, S, stream, tmA, tmW, g, (int)tiles_n, S);
+    return launch_fp8_split_as<NT, true, T>(tmA, tmW, g, chunks, tiles_n, S, stream);
 }
 
 template <int BN, typename T>

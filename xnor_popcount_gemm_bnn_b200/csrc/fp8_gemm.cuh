@@ -43,6 +43,14 @@ __device__ __forceinline__ float fp8_out<float>(float v) { return v; }
 template <>
 __device__ __forceinline__ __nv_bfloat16 fp8_out<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
 
+// Four consecutive outputs, aligned to four elements.
+__device__ __forceinline__ void store4(float* p, float4 v) { *reinterpret_cast<float4*>(p) = v; }
+__device__ __forceinline__ void store4(__nv_bfloat16* p, float4 v) {
+    const __nv_bfloat162 a = __floats2bfloat162_rn(v.x, v.y), b = __floats2bfloat162_rn(v.z, v.w);
+    *reinterpret_cast<uint2*>(p) =
+        make_uint2(reinterpret_cast<const uint32_t&>(a), reinterpret_cast<const uint32_t&>(b));
+}
+
 // Rows [r0, r1) of group e, clamped to [0, R] whatever the offsets hold.
 __device__ __forceinline__ int2 fp8_group_rows(const Fp8Gemm& g, int e) {
     if (g.offsets == nullptr) return make_int2(0, g.R);
@@ -76,14 +84,6 @@ __host__ __device__ constexpr uint32_t f8_idesc(int m, int n) {
     return (1u << 4) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
 }
 
-// tc_wait for waits that come once per K block: the timer is read only after
-// the wait has failed for a while.
-__device__ __forceinline__ bool f8_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
-    #pragma unroll 1
-    for (int i = 0; i < 64; ++i)
-        if (mbar_try_wait(bar, parity)) return true;
-    return tc_wait(bar, parity, abort_flag);
-}
 // True in one lane of a converged warp.  The compiler knows that one lane
 // runs what this guards, and issues tensor-core and copy instructions there
 // without a loop over the lanes.
@@ -96,13 +96,6 @@ __device__ __forceinline__ bool elect_one() {
         : "=r"(p));
     return p != 0;
 }
-// f8_wait by one lane for its warp.
-__device__ __forceinline__ bool f8_wait_warp(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int lane) {
-    int ok = 1;
-    if (lane == 0) ok = f8_wait(bar, parity, abort_flag) ? 1 : 0;
-    return __shfl_sync(0xffffffffu, ok, 0) != 0;
-}
-
 __device__ __forceinline__ void cp_async4(void* dst, const void* src) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
 }
@@ -112,7 +105,9 @@ __device__ __forceinline__ void cp_async_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// f8_wait by all lanes of a converged warp, which stay converged.
+// tc_wait by all lanes of a converged warp, which stay converged, for waits that
+// come once per K block: the timer is read only after the wait has failed for a
+// while.
 __device__ __forceinline__ bool f8_wait_all(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
     #pragma unroll 1
     for (int i = 0; i < 64; ++i)
@@ -135,9 +130,12 @@ __device__ __forceinline__ void fma2(float2& acc, float2 t, float2 s) {
         : "l"(reinterpret_cast<unsigned long long&>(t)), "l"(reinterpret_cast<unsigned long long&>(s)));
 }
 
-__device__ __forceinline__ float ld_shared_cluster_f32(uint32_t addr) {
-    float v;
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+__device__ __forceinline__ float4 ld_shared_cluster_v4(uint32_t addr) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(addr)
+                 : "memory");
     return v;
 }
 __device__ __forceinline__ uint32_t mapa_shared(uint32_t addr, uint32_t rank) {
@@ -152,52 +150,72 @@ __device__ __forceinline__ uint32_t mapa_shared(uint32_t addr, uint32_t rank) {
 namespace f8s {
 constexpr int BN = 128;                      // weight rows per CTA = TMEM lanes
 constexpr int W_BYTES = BN * fp8::BLOCK;     // 16 KiB of weights per stage
-constexpr int WARP_PRODUCER = 0, WARP_MMA = 1, WARP_EPI0 = 2;
-constexpr int THREADS = 6 * 32;
+constexpr int WARP_PRODUCER = 0, WARP_MMA = 1, WARP_SCALE = 2, WARP_EPI0 = 4;
+constexpr int AHEAD = 8;                     // K blocks whose scales are in flight
 constexpr int MAX_SPLIT = 8;
-// Two CTAs share an SM: weights stream from HBM while the other CTA starts or
-// ends.  Never three, so that two always find their tensor memory (see NBUF):
-// a cluster's CTAs wait for one another and must not wait for an allocation.
-constexpr int SMEM_TWO = 113 * 1024;
-template <int NT>
+constexpr int SMEM_SM = 228 * 1024;          // shared memory of an SM, 1 KiB of it reserved per CTA
+template <int NT, bool DEEP>
 struct Cfg {
     static constexpr int STAGE = W_BYTES + NT * fp8::BLOCK;
-    static constexpr int FIXED = 2 * NT * 4 + 512 + 1024;
-    static constexpr int STAGES = (SMEM_TWO - FIXED) / STAGE;
+    static constexpr int NBUF = 4;                           // accumulators in tensor memory
+    static constexpr int TMEM_COLS = NBUF * NT;
+    // CTAs per SM: weights stream from HBM for one while another starts or
+    // ends.  Whatever variants meet on an SM, their shared memory lets no more
+    // in than tensor memory has room for: a cluster's CTAs wait for one another
+    // and must not wait for an allocation.
+    static constexpr int PER_SM = NT <= 64 ? 2 : 1;
+    static constexpr int PARTS = NT <= 64 ? 1 : 2;           // warps per quadrant, each with its columns
+    static constexpr int CW = NT / PARTS;
+    static constexpr int THREADS = (WARP_EPI0 + 4 * PARTS) * 32;
+    static constexpr int SC = (NT + 31) / 32;                // columns per lane of the scale warp
+    static constexpr int RAW_BYTES = AHEAD * (SC + 1) * 32 * 4;
+    static constexpr int PROD_BYTES = 2 * NBUF * NT * 4;
+    static constexpr int FIXED = RAW_BYTES + PROD_BYTES + 512 + 1024;
+    // DEEP: as many stages as fit.  Else three, enough in flight for a short
+    // stream, and room for a CTA of the next launch to set up beside the two of
+    // this one (NT = 16 only, see the launcher).
+    static constexpr int STAGES = DEEP ? (SMEM_SM / PER_SM - 1024 - FIXED) / STAGE : 3;
     static constexpr int SMEM_BYTES = FIXED + STAGES * STAGE;
-    // Accumulators in flight; with two CTAs per SM they fill at most 512 columns.
-    static constexpr int NBUF = NT <= 64 ? 4 : 2;
-    static constexpr int TMEM_COLS = NBUF * NT < 32 ? 32 : NBUF * NT;
-    static_assert(STAGES >= 3 && TMEM_COLS <= 256, "two CTAs per SM");
-    static_assert(3 * (SMEM_BYTES + 1024) > 228 * 1024, "never three CTAs per SM");
+    static_assert(TMEM_COLS >= 32 && (TMEM_COLS & (TMEM_COLS - 1)) == 0 && TMEM_COLS * PER_SM <= 512, "tensor memory");
     static_assert(NT * BN * 4 <= STAGES * STAGE, "the partial sums reuse the ring");
     static_assert(STAGE % 1024 == 0, "128B swizzle");
     static_assert((2 * STAGES + 2 * NBUF + 1) * 8 + 16 <= 512, "barriers");
+    static constexpr int SHARE = SMEM_BYTES + 1024;          // of SMEM_SM
 };
+// What fits together in shared memory has its tensor memory: two CTAs of 256
+// columns leave no room for another, one of 512 for none.
+constexpr int SMALLEST = Cfg<16, false>::SHARE;
+static_assert(SMALLEST <= Cfg<16, true>::SHARE && SMALLEST <= Cfg<32, true>::SHARE &&
+                  2 * Cfg<64, true>::SHARE + SMALLEST > SMEM_SM && Cfg<64, true>::SHARE <= Cfg<32, true>::SHARE &&
+                  Cfg<128, true>::SHARE + SMALLEST > SMEM_SM,
+              "tensor memory of the CTAs that share an SM");
 }  // namespace f8s
 
 // grid: (tiles of 128 weight rows x E) * S CTAs in clusters of S, y over chunks
 // of NT rows (a group's chunks are walked in steps of gridDim.y).  Cluster
 // rank r takes K blocks [r nk / S, (r + 1) nk / S).
 //  warp 0     producer: TMA of 128 weight rows and NT rows of A per K block.
-//  warp 1     one thread issues the block's four MMAs (M = 128, N = NT) and
-//             commits them to the stage and to the accumulator.
-//  warps 2-5  epilogue: thread = one weight row; per block NT accumulators
-//             from tensor memory times sA[b, column] * sW[b, tile], the
-//             products of scales passing through shared memory one block ahead.
+//  warp 1     issues the block's four MMAs (M = 128, N = NT) and commits them
+//             to the accumulator and to the stage.
+//  warp 2     scales: sA[b, column] * sW[b, tile] of the NT columns, copied AHEAD
+//             blocks ahead and put into shared memory; its arrival on the
+//             accumulator's barrier goes with the MMAs' commit.
+//  warps 4 .. epilogue: thread = one weight row; per block its columns' sums
+//             from tensor memory times their scales, added in registers.
 // With S > 1 the CTAs leave their partial sums in shared memory and each adds
 // the columns r, r + S, ... of all of them in rank order: the same sum on every run.
-template <int NT, typename T>
-__global__ void __launch_bounds__(f8s::THREADS)
+template <int NT, bool DEEP, typename T>
+__global__ void __launch_bounds__(f8s::Cfg<NT, DEEP>::THREADS, f8s::Cfg<NT, DEEP>::PER_SM)
 fp8_gemm_split_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmW, Fp8Gemm g,
-                      int tiles_n, int S) {
+                      int tiles_n, int S, int vec_out) {
     using namespace f8s;
-    using C = Cfg<NT>;
-    constexpr int STAGES = C::STAGES, NBUF = C::NBUF;
+    using C = Cfg<NT, DEEP>;
+    constexpr int STAGES = C::STAGES, NBUF = C::NBUF, SC = C::SC, CW = C::CW;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* ring = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-    float* sbuf = reinterpret_cast<float*>(ring + STAGES * C::STAGE);      // [2][NT]
-    uint64_t* full = reinterpret_cast<uint64_t*>(sbuf + 2 * NT);
+    float* prod = reinterpret_cast<float*>(ring + STAGES * C::STAGE);      // [2 NBUF][NT]
+    float* raw = prod + C::PROD_BYTES / 4;                                 // [AHEAD][SC + 1][32]
+    uint64_t* full = reinterpret_cast<uint64_t*>(raw + C::RAW_BYTES / 4);
     uint64_t* empty = full + STAGES;
     uint64_t* tfull = empty + STAGES;
     uint64_t* tempty = tfull + NBUF;
@@ -219,8 +237,8 @@ fp8_gemm_split_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_cons
             mbar_init(&empty[s], 1);
         }
         for (int b = 0; b < NBUF; ++b) {
-            mbar_init(&tfull[b], 1);
-            mbar_init(&tempty[b], 4);
+            mbar_init(&tfull[b], 2);                   // the MMAs' commit and the scales
+            mbar_init(&tempty[b], 4 * C::PARTS);
         }
         mbar_init(drain, 1);
         *abort_flag = 0;
@@ -247,7 +265,7 @@ fp8_gemm_split_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_cons
         if (warp == WARP_PRODUCER) {
             for (int kb = kb0; ok && kb < kb1; ++kb, ++it) {
                 const uint32_t s = it % STAGES;
-                ok = it < STAGES || f8_wait_warp(&empty[s], ((it / STAGES) - 1) & 1, abort_flag, lane);
+                ok = it < STAGES || f8_wait_all(&empty[s], ((it / STAGES) - 1) & 1, abort_flag);
                 if (!ok) break;
                 if (elect_one()) {
                     uint8_t* dst = ring + s * C::STAGE;
@@ -264,97 +282,139 @@ fp8_gemm_split_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_cons
             const uint64_t wdesc = umma_desc_sw128(smem_u32(ring));
             for (int kb = kb0; ok && kb < kb1; ++kb, ++it) {
                 const uint32_t s = it % STAGES, b = it % NBUF;
-                ok = (it < NBUF || f8_wait_warp(&tempty[b], ((it / NBUF) - 1) & 1, abort_flag, lane)) &&
-                     f8_wait_warp(&full[s], (it / STAGES) & 1, abort_flag, lane);
+                const uint64_t dw = wdesc + (uint64_t)(s * (C::STAGE >> 4)), da = dw + (W_BYTES >> 4);
+                ok = f8_wait_all(&full[s], (it / STAGES) & 1, abort_flag) &&
+                     (it < NBUF || f8_wait_all(&tempty[b], ((it / NBUF) - 1) & 1, abort_flag));
                 if (!ok) break;
                 tc_fence_after();
                 if (elect_one()) {
-                    const uint64_t dw = wdesc + (uint64_t)(s * (C::STAGE >> 4)), da = dw + (W_BYTES >> 4);
                     #pragma unroll
                     for (int kk = 0; kk < 4; ++kk)
                         mma_f8<1>(tmem_base + b * NT, dw + kk * 2, da + kk * 2, f8_idesc(BN, NT), kk != 0 ? 1u : 0u);
-                    mma_commit(&empty[s]);
                     mma_commit(&tfull[b]);
+                    mma_commit(&empty[s]);
                 }
                 __syncwarp();
             }
-        } else {
-            const int quad = warp & 3, tid = (int)threadIdx.x - WARP_EPI0 * 32;
-            const int cols = min(NT, rows.y - m0);
-            const bool mine = tid < cols;
-            const float* sa = g.sa + m0 + tid;
+        } else if (warp == WARP_SCALE) {
+            const float* sa = g.sa + m0 + lane;
             const float* sw = g.sw + e * g.sw_stride + tile;
-            auto scale = [&](int kb) { return mine && kb < kb1 ? sa[kb * g.ldsa] * sw[kb * g.ldsw] : 0.0f; };
-            float2 acc[NT / 2];
-            #pragma unroll
-            for (int c = 0; c < NT / 2; ++c) acc[c] = make_float2(0.0f, 0.0f);
-            if (tid < NT) sbuf[tid] = scale(kb0);
-            float next = scale(kb0 + 1);
-            named_bar_sync(f4::EPI_BAR, 128);
-            for (int kb = kb0; kb < kb1; ++kb, ++it) {
-                const uint32_t b = it % NBUF;
-                const float* s = sbuf + ((kb - kb0) & 1) * NT;
-                ok = ok && f8_wait_warp(&tfull[b], (it / NBUF) & 1, abort_flag, lane);
-                if (ok) {
-                    tc_fence_after();
-                    const uint32_t t0 = tmem_base + ((uint32_t)(32 * quad) << 16) + b * NT;
-                    constexpr int CH = NT < 32 ? 16 : 32;
+            const int cols = rows.y - m0;
+            // Every lane copies what it needs itself, so only its own copies
+            // are waited for; columns past the group's end keep what the slot
+            // held (their sums are not stored).
+            auto load = [&](int kb) {
+                if (kb < kb1) {
+                    float* d = raw + ((kb - kb0) % AHEAD) * (SC + 1) * 32 + lane;
                     #pragma unroll
-                    for (int c = 0; c < NT; c += CH) {
-                        uint32_t r[CH];
-                        if constexpr (CH == 16) tmem_ld16_sync(t0 + c, r);
-                        else tmem_ld32_sync(t0 + c, r);
-                        if (c + CH == NT) {
-                            tc_fence_before();
-                            __syncwarp();
-                            if (lane == 0) mbar_arrive(&tempty[b]);
-                        }
-                        #pragma unroll
-                        for (int j = 0; j < CH; j += 4) {
-                            const float4 f = *reinterpret_cast<const float4*>(s + c + j);
-                            fma2(acc[(c + j) / 2], make_float2(__uint_as_float(r[j]), __uint_as_float(r[j + 1])),
-                                 make_float2(f.x, f.y));
-                            fma2(acc[(c + j) / 2 + 1],
-                                 make_float2(__uint_as_float(r[j + 2]), __uint_as_float(r[j + 3])),
-                                 make_float2(f.z, f.w));
-                        }
+                    for (int i = 0; i < SC; ++i)
+                        if (32 * i + lane < min(cols, NT)) cp_async4(d + 32 * i, sa + kb * g.ldsa + 32 * i);
+                    cp_async4(d + 32 * SC, sw + kb * g.ldsw);
+                }
+                cp_async_commit();
+            };
+            #pragma unroll
+            for (int i = 0; i < AHEAD - 1; ++i) load(kb0 + i);
+            for (int kb = kb0; ok && kb < kb1; ++kb, ++it) {
+                const uint32_t b = it % NBUF;
+                load(kb + AHEAD - 1);
+                cp_async_wait<AHEAD - 1>();
+                // The accumulator's previous use is committed: its barrier can
+                // take this block's arrival, and the epilogue is done with the
+                // block 2 NBUF before this one (the MMAs had waited for it).
+                ok = it < NBUF || f8_wait_all(&tfull[b], ((it / NBUF) - 1) & 1, abort_flag);
+                if (!ok) break;
+                const float* d = raw + ((kb - kb0) % AHEAD) * (SC + 1) * 32 + lane;
+                float* p = prod + (it % (2 * NBUF)) * NT + lane;
+                const float w = d[32 * SC];
+                #pragma unroll
+                for (int i = 0; i < SC; ++i)
+                    if (32 * i + lane < NT) p[32 * i] = d[32 * i] * w;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&tfull[b]);
+            }
+            cp_async_wait<0>();
+        } else if (warp >= WARP_EPI0) {
+            const int quad = warp & 3, part = (warp - WARP_EPI0) >> 2;
+            const int cols = min(NT, rows.y - m0);
+            const uint32_t tq = tmem_base + ((uint32_t)(32 * quad) << 16) + part * CW;
+            constexpr int CH = CW < 32 ? CW : 32;           // columns per load
+            float2 acc[CW / 2];
+            #pragma unroll
+            for (int c = 0; c < CW / 2; ++c) acc[c] = make_float2(0.0f, 0.0f);
+            #pragma unroll 1
+            for (int kb = kb0; ok && kb < kb1; ++kb, ++it) {
+                const uint32_t b = it % NBUF;
+                ok = f8_wait_all(&tfull[b], (it / NBUF) & 1, abort_flag);
+                if (!ok) break;
+                tc_fence_after();
+                const float* s = prod + (it % (2 * NBUF)) * NT + part * CW;
+                #pragma unroll
+                for (int c = 0; c < CW; c += CH) {
+                    uint32_t r[CH];
+                    if constexpr (CH == 16) tmem_ld16_sync(tq + b * NT + c, r);
+                    else tmem_ld32_sync(tq + b * NT + c, r);
+                    #pragma unroll
+                    for (int j = 0; j < CH; j += 4) {
+                        const float4 f = *reinterpret_cast<const float4*>(s + c + j);
+                        fma2(acc[(c + j) / 2], make_float2(__uint_as_float(r[j]), __uint_as_float(r[j + 1])),
+                             make_float2(f.x, f.y));
+                        fma2(acc[(c + j) / 2 + 1], make_float2(__uint_as_float(r[j + 2]), __uint_as_float(r[j + 3])),
+                             make_float2(f.z, f.w));
                     }
                 }
-                if (tid < NT) sbuf[((kb - kb0 + 1) & 1) * NT + tid] = next;
-                next = scale(kb + 2);
-                named_bar_sync(f4::EPI_BAR, 128);
+                tc_fence_before();
+                __syncwarp();                       // every lane has used its scales
+                if (elect_one()) mbar_arrive(&tempty[b]);
             }
             const int n = 32 * quad + lane;
             T* out = static_cast<T*>(g.out) + n0 + n;
             if (S == 1) {
                 if (ok && n0 + n < g.N) {
                     #pragma unroll
-                    for (int c = 0; c < NT; ++c)
-                        if (c < cols) out[(int64_t)(m0 + c) * g.ldo] = fp8_out<T>(c & 1 ? acc[c / 2].y : acc[c / 2].x);
+                    for (int c = 0; c < CW; ++c) {
+                        const int m = part * CW + c;
+                        if (m < cols) out[(int64_t)(m0 + m) * g.ldo] = fp8_out<T>(c & 1 ? acc[c / 2].y : acc[c / 2].x);
+                    }
                 }
             } else {
-                // All MMAs of this chunk are done (their accumulators were
-                // read), so the ring is free for the partial sums.
-                float* part = reinterpret_cast<float*>(ring);
+                // The last block's commit covers all MMAs of this chunk, so the
+                // ring is free for the partial sums.
+                float* sum = reinterpret_cast<float*>(ring) + part * CW * BN + n;
                 #pragma unroll
-                for (int c = 0; c < NT; ++c) part[c * BN + n] = c & 1 ? acc[c / 2].y : acc[c / 2].x;
+                for (int c = 0; c < CW; ++c)
+                    if (part * CW + c < cols) sum[c * BN] = c & 1 ? acc[c / 2].y : acc[c / 2].x;
             }
         }
         if (S > 1) {
             __syncwarp();
             cluster_sync_all();
             if (warp >= WARP_EPI0) {
-                const int n = (int)threadIdx.x - WARP_EPI0 * 32, cols = min(NT, rows.y - m0);
-                T* out = static_cast<T*>(g.out) + n0 + n;
-                for (int c = rank; c < cols; c += S) {
-                    float v[MAX_SPLIT];
+                // A warp takes whole columns, four rows of weights per lane.
+                const int n = n0 + 4 * lane, cols = min(NT, rows.y - m0);
+                for (int c = rank + (warp - WARP_EPI0) * S; c < cols; c += 4 * C::PARTS * S) {
+                    const uint32_t at = smem_u32(ring) + (c * BN + 4 * lane) * 4;
+                    float4 v[MAX_SPLIT];
                     #pragma unroll
-                    for (int r = 0; r < MAX_SPLIT; ++r)
-                        v[r] = r < S ? ld_shared_cluster_f32(mapa_shared(smem_u32(ring) + (c * BN + n) * 4, r)) : 0.0f;
-                    float y = v[0];
+                    for (int r = 0; r < MAX_SPLIT; ++r) v[r] = ld_shared_cluster_v4(mapa_shared(at, min(r, S - 1)));
+                    float4 y = v[0];
                     #pragma unroll
-                    for (int r = 1; r < MAX_SPLIT; ++r) y += v[r];
-                    if (ok && n0 + n < g.N) out[(int64_t)(m0 + c) * g.ldo] = fp8_out<T>(y);
+                    for (int r = 1; r < MAX_SPLIT; ++r) {
+                        y.x += r < S ? v[r].x : 0.0f;
+                        y.y += r < S ? v[r].y : 0.0f;
+                        y.z += r < S ? v[r].z : 0.0f;
+                        y.w += r < S ? v[r].w : 0.0f;
+                    }
+                    T* out = static_cast<T*>(g.out) + (int64_t)(m0 + c) * g.ldo + n;
+                    if (!ok) continue;
+                    if (vec_out && n + 4 <= g.N) {
+                        store4(out, y);
+                    } else {
+                        if (n < g.N) out[0] = fp8_out<T>(y.x);
+                        if (n + 1 < g.N) out[1] = fp8_out<T>(y.y);
+                        if (n + 2 < g.N) out[2] = fp8_out<T>(y.z);
+                        if (n + 3 < g.N) out[3] = fp8_out<T>(y.w);
+                    }
                 }
                 // Ordered before the next chunk's copies into the ring.
                 fence_proxy_async_shared();
@@ -559,7 +619,7 @@ fp8_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
         for (int t = cid; ok && tiles.find(g, lane, t, tl); t += ncl) {
             for (int kb = 0; kb < nk; ++kb, ++it) {
                 const uint32_t s = it % STAGES;
-                ok = it < STAGES || f8_wait_warp(&empty[s], ((it / STAGES) - 1) & 1, abort_flag, lane);
+                ok = it < STAGES || f8_wait_all(&empty[s], ((it / STAGES) - 1) & 1, abort_flag);
                 if (!ok) break;
                 if (elect_one()) {
                     uint8_t* dst = ring + s * C::STAGE;
