@@ -1916,16 +1916,20 @@ bnn_status launch_fp8_gemm(const Fp8Operands& o, const bnn::Fp8Gemm& g, int out_
 }
 
 template <typename T, int ALIGN>
-void launch_fp8_pack(const void* x, int64_t x_rows, int64_t K, int64_t ld_x, const int32_t* row_index, int64_t rows,
-                     int block_rows, uint8_t* codes, int64_t ldc, float* scales, int64_t lds, unsigned grid,
-                     int64_t tasks, cudaStream_t stream) {
+bnn_status launch_fp8_pack(const void* x, int64_t x_rows, int64_t K, int64_t ld_x, const int32_t* row_index,
+                           int64_t rows, int block_rows, uint8_t* codes, int64_t ldc, float* scales, int64_t lds,
+                           cudaStream_t stream) {
     const T* xt = static_cast<const T*>(x);
-    if (block_rows == 1)
-        bnn::fp8_pack_rows_kernel<T, ALIGN, 2><<<grid, 256, 0, stream>>>(xt, x_rows, K, ld_x, row_index, rows, codes,
-                                                                         ldc, scales, lds, tasks);
-    else
-        bnn::fp8_pack_blocks_kernel<T, ALIGN><<<grid, 256, 0, stream>>>(xt, rows, K, ld_x, codes, ldc, scales, lds,
-                                                                        ceil_div(K, bnn::fp8::BLOCK));
+    constexpr int U = sizeof(T) == 2 ? 2 : 1;               // 32 registers of loads in flight per lane
+    if (block_rows == 1) {
+        const dim3 grid((unsigned)ceil_div(rows, 8), (unsigned)std::min<int64_t>(ceil_div(K, 512 * U), 65535));
+        return launch_clusters(bnn::fp8_pack_rows_kernel<T, ALIGN, U>, grid, 256, 0, 1, stream, xt, x_rows, K, ld_x,
+                               row_index, rows, codes, ldc, scales, lds);
+    }
+    const int64_t kblocks = ceil_div(K, bnn::fp8::BLOCK), blocks = ceil_div(rows, bnn::fp8::BLOCK) * kblocks;
+    if (blocks > INT_MAX) return BNN_ERR_UNSUPPORTED;
+    return launch_clusters(bnn::fp8_pack_blocks_kernel<T, ALIGN>, dim3((unsigned)blocks), 256, 0, 1, stream, xt, rows,
+                           K, ld_x, codes, ldc, scales, lds, (unsigned)kblocks);
 }
 
 template <typename T>
@@ -1968,28 +1972,14 @@ bnn_status bnn_fp8_pack(const void* x, bnn_dtype dt, int64_t x_rows, int64_t K, 
         return BNN_ERR_ALIGNMENT;
     if (row_index != nullptr && block_rows != 1) return BNN_ERR_UNSUPPORTED;
     if (rows == 0) return BNN_OK;
-    const int64_t es = dtype_bytes(dt);
-    // Rows kernel: a warp takes two 16-byte vectors per lane of one row.
-    const int64_t tasks = rows * ceil_div(K, 2 * 32 * (16 / es));
-    const int64_t grid = block_rows == 1 ? ceil_div(tasks, 8) : ceil_div(rows, BLOCK) * ceil_div(K, BLOCK);
-    if (grid > INT_MAX) return BNN_ERR_UNSUPPORTED;
-    const int64_t row_bytes = ld_x * es;
+    const int64_t row_bytes = ld_x * dtype_bytes(dt);
     const int a = aligned(x, 16) && row_bytes % 16 == 0 ? 16 : aligned(x, 8) && row_bytes % 8 == 0 ? 8 : 4;
     cudaStream_t s = as_cuda(stream);
 #define BNN_PACK(T, A) \
-    launch_fp8_pack<T, A>(x, x_rows, K, ld_x, row_index, rows, block_rows, codes, ld_codes, scales, ld_scales, \
-                          (unsigned)grid, tasks, s)
-    if (dt == BNN_F32) {
-        if (a == 16) BNN_PACK(float, 16);
-        else if (a == 8) BNN_PACK(float, 8);
-        else BNN_PACK(float, 4);
-    } else {
-        if (a == 16) BNN_PACK(__nv_bfloat16, 16);
-        else if (a == 8) BNN_PACK(__nv_bfloat16, 8);
-        else BNN_PACK(__nv_bfloat16, 4);
-    }
+    launch_fp8_pack<T, A>(x, x_rows, K, ld_x, row_index, rows, block_rows, codes, ld_codes, scales, ld_scales, s)
+    if (dt == BNN_F32) return a == 16 ? BNN_PACK(float, 16) : a == 8 ? BNN_PACK(float, 8) : BNN_PACK(float, 4);
+    return a == 16 ? BNN_PACK(__nv_bfloat16, 16) : a == 8 ? BNN_PACK(__nv_bfloat16, 8) : BNN_PACK(__nv_bfloat16, 4);
 #undef BNN_PACK
-    return launch_status();
 }
 
 bnn_status bnn_fp8_gemm(const uint8_t* A, int64_t lda, const float* a_scales, int64_t ld_as, const uint8_t* W,

@@ -22,106 +22,145 @@ constexpr int BLOCK = 128;                  // elements of K (and weight rows) p
 constexpr float CODE_MAX = 448.0f;
 constexpr float SCALE_MIN = 1.17549435e-38f;   // 2^-126: the reciprocal stays finite
 
-// Magnitude bits of a finite value, 0 for infinities and NaN: ordered as
-// unsigned integers exactly as the magnitudes are.
-__device__ __forceinline__ uint32_t finite_abs_bits(float v) {
-    const uint32_t a = __float_as_uint(v) & 0x7FFFFFFFu;
-    return a < 0x7F800000u ? a : 0u;
+__device__ __forceinline__ float block_scale(float amax) { return fmaxf(__fdiv_rn(amax, CODE_MAX), SCALE_MIN); }
+
+// Two codes of a, b (a in the low byte); NaN gives the NaN code.
+__device__ __forceinline__ uint32_t codes2(float a, float b) {
+    return (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
 }
 
-__device__ __forceinline__ float block_scale(uint32_t amax_bits) {
-    return fmaxf(__fdiv_rn(__uint_as_float(amax_bits), CODE_MAX), SCALE_MIN);
-}
+// What a lane packs at a time: 16 consecutive elements as loaded (fp32, or
+// pairs of bf16), an eighth of a block.
+template <typename T>
+struct Elems {
+    static constexpr int WORDS = 16 * (int)sizeof(T) / 4;
+    uint32_t w[WORDS];
 
-// Two codes of a, b times inv (a in the low byte).  x * 0 is 0 for a finite x
-// and NaN for an infinity or NaN, so those become the NaN code and not 448.
-__device__ __forceinline__ uint32_t codes2(float a, float b, float inv) {
-    const float2 q = make_float2(fmaf(a, 0.0f, a * inv), fmaf(b, 0.0f, b * inv));
-    return (uint32_t)__nv_cvt_float2_to_fp8x2(q, __NV_SATFINITE, __NV_E4M3);
-}
-__device__ __forceinline__ uint32_t codes4(const float* v, float inv) {
-    return codes2(v[0], v[1], inv) | (codes2(v[2], v[3], inv) << 16);
-}
-
-// E = 16 / sizeof(T) consecutive elements from column c of a row of K (0 past
-// K).  ALIGN: the alignment in bytes that the row start and c * sizeof(T)
-// share (16, 8, or sizeof(T)).
-template <typename T, int ALIGN>
-__device__ __forceinline__ void load_elems(const T* row, int64_t c, int64_t K, float (&v)[16 / sizeof(T)]) {
-    constexpr int E = 16 / (int)sizeof(T);
-    if (ALIGN >= 8 && c + E <= K) {
-        uint32_t w[4];
-        if constexpr (ALIGN == 16) {
-            const uint4 q = ldg_stream_v4(row + c);
-            w[0] = q.x; w[1] = q.y; w[2] = q.z; w[3] = q.w;
+    // Elements c .. c + 15 of a row of K, 0 past K.  ALIGN: the alignment in
+    // bytes that the row's start and c * sizeof(T) share (16, 8, or less).
+    template <int ALIGN>
+    __device__ __forceinline__ void load(const T* row, int64_t c, int64_t K) {
+        if (ALIGN >= 8 && c + 16 <= K) {
+            if constexpr (ALIGN == 16) {
+                #pragma unroll
+                for (int i = 0; i < WORDS; i += 4) {
+                    const uint4 q = ldg_stream_v4(reinterpret_cast<const uint32_t*>(row + c) + i);
+                    w[i] = q.x; w[i + 1] = q.y; w[i + 2] = q.z; w[i + 3] = q.w;
+                }
+            } else {
+                #pragma unroll
+                for (int i = 0; i < WORDS; i += 2) {
+                    const uint2 q = __ldg(reinterpret_cast<const uint2*>(row + c) + i / 2);
+                    w[i] = q.x; w[i + 1] = q.y;
+                }
+            }
         } else {
-            const uint2 p = __ldg(reinterpret_cast<const uint2*>(row + c));
-            const uint2 q = __ldg(reinterpret_cast<const uint2*>(row + c) + 1);
-            w[0] = p.x; w[1] = p.y; w[2] = q.x; w[3] = q.y;
+            #pragma unroll
+            for (int i = 0; i < WORDS; ++i) {
+                if constexpr (sizeof(T) == 4) {
+                    w[i] = c + i < K ? __float_as_uint(to_float(row[c + i])) : 0u;
+                } else {
+                    const uint32_t lo = c + 2 * i < K ? __bfloat16_as_ushort(row[c + 2 * i]) : 0u;
+                    const uint32_t hi = c + 2 * i + 1 < K ? __bfloat16_as_ushort(row[c + 2 * i + 1]) : 0u;
+                    w[i] = lo | (hi << 16);
+                }
+            }
         }
-        #pragma unroll
-        for (int i = 0; i < E; ++i) {
-            if constexpr (sizeof(T) == 4) v[i] = __uint_as_float(w[i]);
-            else v[i] = __uint_as_float((i & 1) ? (w[i >> 1] & 0xFFFF0000u) : (w[i >> 1] << 16));
-        }
-    } else {
-        #pragma unroll
-        for (int i = 0; i < E; ++i) v[i] = c + i < K ? to_float(row[c + i]) : 0.0f;
     }
-}
+    __device__ __forceinline__ float value(int i) const {
+        if constexpr (sizeof(T) == 4) return __uint_as_float(w[i]);
+        else return __uint_as_float((i & 1) ? (w[i >> 1] & 0xFFFF0000u) : (w[i >> 1] << 16));
+    }
+    // Largest |x|: NaN left out (unless all are), infinities not.
+    __device__ __forceinline__ float amax() const {
+        if constexpr (sizeof(T) == 4) {
+            float a = fabsf(value(0));
+            #pragma unroll
+            for (int i = 1; i < 16; ++i) a = fmaxf(a, fabsf(value(i)));
+            return a;
+        } else {
+            __nv_bfloat162 a = __habs2(reinterpret_cast<const __nv_bfloat162&>(w[0]));
+            #pragma unroll
+            for (int i = 1; i < WORDS; ++i) a = __hmax2(a, __habs2(reinterpret_cast<const __nv_bfloat162&>(w[i])));
+            return fmaxf(__low2float(a), __high2float(a));
+        }
+    }
+    __device__ __forceinline__ float finite_amax() const {
+        float a = 0.0f;
+        #pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const float v = fabsf(value(i));
+            if (v < __int_as_float(0x7F800000)) a = fmaxf(a, v);
+        }
+        return a;
+    }
+    // 16 codes of x * inv.  SPECIAL (the block holds an infinity): x * 0 is 0
+    // for a finite x and NaN for an infinity, which then gets the NaN code.
+    template <bool SPECIAL>
+    __device__ __forceinline__ uint4 codes(float inv) const {
+        uint32_t o[4];
+        #pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            float q[4];
+            #pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float v = value(4 * i + j);
+                q[j] = SPECIAL ? fmaf(v, 0.0f, v * inv) : v * inv;
+            }
+            o[i] = codes2(q[0], q[1]) | (codes2(q[2], q[3]) << 16);
+        }
+        return make_uint4(o[0], o[1], o[2], o[3]);
+    }
+};
 
-// E codes at column c of a code row (ld a multiple of 16, so 4- and 8-byte
-// stores are aligned); columns from kp (K rounded up to 16) on stay unwritten.
-template <int E>
-__device__ __forceinline__ void store_codes(uint8_t* row, int64_t c, int64_t kp, const float (&v)[E], float inv) {
-    if (c >= kp) return;
-    if constexpr (E == 8) {
-        *reinterpret_cast<uint2*>(row + c) = make_uint2(codes4(v, inv), codes4(v + 4, inv));
-    } else {
-        *reinterpret_cast<uint32_t*>(row + c) = codes4(v, inv);
-    }
-}
+// No number, or an infinity.
+__device__ __forceinline__ bool not_finite(float a) { return !(a < __int_as_float(0x7F800000)); }
+constexpr int LANES = BLOCK / 16;           // lanes per block of a row
 }  // namespace fp8
 
-// Blocks of 1 x 128.  A warp takes U vectors of one row (a 16-byte vector per
-// lane: 256 bf16 or 128 fp32 elements per vector); the 16 (or 32) lanes of a
-// block find its amax by shuffles, and every element is read once.  Warps of
-// consecutive rows run next to each other, so their scales, consecutive in
-// memory, meet in L2.
+// Blocks of 1 x 128.  Eight lanes share a block; a warp takes U x 512 elements
+// of one row and reads every element once.  Warps of consecutive rows run next
+// to each other, so their scales, consecutive in memory, meet in L2.  Bound by
+// memory: about 70 instructions per 16 elements, few enough at 2 bytes each.
 template <typename T, int ALIGN, int U>
 __global__ void __launch_bounds__(256)
 fp8_pack_rows_kernel(const T* __restrict__ x, int64_t x_rows, int64_t K, int64_t ld_x,
                      const int32_t* __restrict__ row_index, int64_t rows, uint8_t* __restrict__ codes, int64_t ldc,
-                     float* __restrict__ scales, int64_t lds, int64_t tasks) {
+                     float* __restrict__ scales, int64_t lds) {
     using namespace fp8;
-    constexpr int E = 16 / (int)sizeof(T);
-    constexpr int LANES = BLOCK / E;                 // lanes per block
+    grid_dependency_wait();
+    grid_dependents_launch();
     const int lane = threadIdx.x & 31;
-    const int64_t task = (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
-    if (task >= tasks) return;
-    const int64_t r = task % rows;
-    const int64_t c0 = task / rows * (32 * E * U);
+    const int64_t r = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+    if (r >= rows) return;
     int64_t src = r;
     if (row_index != nullptr) {
         src = __ldg(row_index + r);
         if (src < 0 || src >= x_rows) return;        // the row is left as it was
     }
     const T* xr = x + src * ld_x;
-    const int64_t kp = (K + 15) / 16 * 16;
-    float v[U][E];
-    #pragma unroll
-    for (int u = 0; u < U; ++u) load_elems<T, ALIGN>(xr, c0 + (u * 32 + lane) * E, K, v[u]);
-    #pragma unroll
-    for (int u = 0; u < U; ++u) {
-        const int64_t c = c0 + (u * 32 + lane) * E;
-        uint32_t a = 0;
+    for (int64_t c0 = (int64_t)blockIdx.y * (512 * U) + lane * 16; c0 - lane * 16 < K; c0 += (int64_t)gridDim.y * (512 * U)) {
+        Elems<T> v[U];
         #pragma unroll
-        for (int i = 0; i < E; ++i) a = max(a, finite_abs_bits(v[u][i]));
+        for (int u = 0; u < U; ++u) v[u].template load<ALIGN>(xr, c0 + u * 512, K);
         #pragma unroll
-        for (int off = 1; off < LANES; off <<= 1) a = max(a, __shfl_xor_sync(0xffffffffu, a, off));
-        const float s = block_scale(a);
-        store_codes<E>(codes + r * ldc, c, kp, v[u], __frcp_rn(s));
-        if ((lane & (LANES - 1)) == 0 && c < K) scales[c / BLOCK * lds + r] = s;
+        for (int u = 0; u < U; ++u) {
+            const int64_t c = c0 + u * 512;
+            float a = v[u].amax();
+            #pragma unroll
+            for (int off = 1; off < LANES; off <<= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, off));
+            const bool special = __any_sync(0xffffffffu, not_finite(a));
+            if (special) {
+                a = v[u].finite_amax();
+                #pragma unroll
+                for (int off = 1; off < LANES; off <<= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, off));
+            }
+            const float s = block_scale(a), inv = __frcp_rn(s);
+            if (c >= K) continue;
+            *reinterpret_cast<uint4*>(codes + r * ldc + c) =
+                special ? v[u].template codes<true>(inv) : v[u].template codes<false>(inv);
+            if ((lane & (LANES - 1)) == 0) scales[c / BLOCK * lds + r] = s;
+        }
     }
 }
 
@@ -130,46 +169,42 @@ fp8_pack_rows_kernel(const T* __restrict__ x, int64_t x_rows, int64_t K, int64_t
 template <typename T, int ALIGN>
 __global__ void __launch_bounds__(256)
 fp8_pack_blocks_kernel(const T* __restrict__ x, int64_t rows, int64_t K, int64_t ld_x, uint8_t* __restrict__ codes,
-                       int64_t ldc, float* __restrict__ scales, int64_t lds, int64_t kblocks) {
+                       int64_t ldc, float* __restrict__ scales, int64_t lds, unsigned kblocks) {
     using namespace fp8;
-    constexpr int E = 16 / (int)sizeof(T);
-    constexpr int LANES = BLOCK / E;                 // lanes per row of the block
-    constexpr int RPW = 32 / LANES;                  // rows per warp and vector
-    constexpr int U = BLOCK / (8 * RPW);             // vectors per lane
-    __shared__ uint32_t part[8];
+    constexpr int U = 4;                             // passes of 8 warps x 4 rows
+    __shared__ float part[8];
+    grid_dependency_wait();
+    grid_dependents_launch();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t kb = blockIdx.x % kblocks, rb = blockIdx.x / kblocks;
-    const int64_t c = kb * BLOCK + (lane & (LANES - 1)) * E;
-    const int64_t r0 = rb * BLOCK + warp * (U * RPW) + lane / LANES;
-    const int64_t kp = (K + 15) / 16 * 16;
-    float v[U][E];
+    const int64_t c = kb * BLOCK + (lane & (LANES - 1)) * 16;
+    const int64_t r0 = rb * BLOCK + warp * 4 + lane / LANES;
+    Elems<T> v[U];
     #pragma unroll
-    for (int u = 0; u < U; ++u) {
-        const int64_t r = r0 + u * RPW;
-        if (r < rows) {
-            load_elems<T, ALIGN>(x + r * ld_x, c, K, v[u]);
-        } else {
-            #pragma unroll
-            for (int i = 0; i < E; ++i) v[u][i] = 0.0f;
-        }
-    }
-    uint32_t a = 0;
+    for (int u = 0; u < U; ++u) v[u].template load<ALIGN>(x + min(r0 + 32 * u, rows - 1) * ld_x, c, K);
+    // A row past the end is read as the last one: its elements change no amax
+    // of a block that holds that row.
+    float a = v[0].amax();
     #pragma unroll
-    for (int u = 0; u < U; ++u) {
+    for (int u = 1; u < U; ++u) a = fmaxf(a, v[u].amax());
+    bool special = __syncthreads_or(not_finite(a));
+    if (special) {
+        a = 0.0f;
         #pragma unroll
-        for (int i = 0; i < E; ++i) a = max(a, finite_abs_bits(v[u][i]));
+        for (int u = 0; u < U; ++u) a = fmaxf(a, v[u].finite_amax());
     }
-    a = __reduce_max_sync(0xffffffffu, a);
+    a = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(a)));   // magnitudes order as integers
     if (lane == 0) part[warp] = a;
     __syncthreads();
     #pragma unroll
-    for (int w = 0; w < 8; ++w) a = max(a, part[w]);
-    const float s = block_scale(a);
-    const float inv = __frcp_rn(s);
+    for (int w = 0; w < 8; ++w) a = fmaxf(a, part[w]);
+    const float s = block_scale(a), inv = __frcp_rn(s);
     #pragma unroll
     for (int u = 0; u < U; ++u) {
-        const int64_t r = r0 + u * RPW;
-        if (r < rows) store_codes<E>(codes + r * ldc, c, kp, v[u], inv);
+        const int64_t r = r0 + 32 * u;
+        if (r < rows && c < K)
+            *reinterpret_cast<uint4*>(codes + r * ldc + c) =
+                special ? v[u].template codes<true>(inv) : v[u].template codes<false>(inv);
     }
     if (threadIdx.x == 0) scales[kb * lds + rb] = s;
 }
