@@ -1920,11 +1920,15 @@ bnn_status launch_fp8_pack(const void* x, int64_t x_rows, int64_t K, int64_t ld_
                            int64_t rows, int block_rows, uint8_t* codes, int64_t ldc, float* scales, int64_t lds,
                            cudaStream_t stream) {
     const T* xt = static_cast<const T*>(x);
-    constexpr int U = sizeof(T) == 2 ? 2 : 1;               // 32 registers of loads in flight per lane
     if (block_rows == 1) {
-        const dim3 grid((unsigned)ceil_div(rows, 8), (unsigned)std::min<int64_t>(ceil_div(K, 512 * U), 65535));
-        return launch_clusters(bnn::fp8_pack_rows_kernel<T, ALIGN, U>, grid, 256, 0, 1, stream, xt, x_rows, K, ld_x,
-                               row_index, rows, codes, ldc, scales, lds);
+        // Four (fp32: two) vectors per lane share the scale's division; when
+        // that leaves the SMs without warps, one each.
+        constexpr int U = sizeof(T) == 2 ? 4 : 2;
+        const bool many = rows * ceil_div(K, 512 * U) >= 16 * (int64_t)sm_count();
+        const dim3 grid((unsigned)ceil_div(rows, 8),
+                        (unsigned)std::min<int64_t>(ceil_div(K, 512 * (many ? U : 1)), 65535));
+        return launch_clusters(many ? bnn::fp8_pack_rows_kernel<T, ALIGN, U> : bnn::fp8_pack_rows_kernel<T, ALIGN, 1>,
+                               grid, 256, 0, 1, stream, xt, x_rows, K, ld_x, row_index, rows, codes, ldc, scales, lds);
     }
     const int64_t kblocks = ceil_div(K, bnn::fp8::BLOCK), blocks = ceil_div(rows, bnn::fp8::BLOCK) * kblocks;
     if (blocks > INT_MAX) return BNN_ERR_UNSUPPORTED;
@@ -1973,12 +1977,17 @@ bnn_status bnn_fp8_pack(const void* x, bnn_dtype dt, int64_t x_rows, int64_t K, 
     if (row_index != nullptr && block_rows != 1) return BNN_ERR_UNSUPPORTED;
     if (rows == 0) return BNN_OK;
     const int64_t row_bytes = ld_x * dtype_bytes(dt);
-    const int a = aligned(x, 16) && row_bytes % 16 == 0 ? 16 : aligned(x, 8) && row_bytes % 8 == 0 ? 8 : 4;
+    int a = 32;
+    while (a > 4 && !(aligned(x, (uintptr_t)a) && row_bytes % a == 0)) a >>= 1;
     cudaStream_t s = as_cuda(stream);
 #define BNN_PACK(T, A) \
     launch_fp8_pack<T, A>(x, x_rows, K, ld_x, row_index, rows, block_rows, codes, ld_codes, scales, ld_scales, s)
-    if (dt == BNN_F32) return a == 16 ? BNN_PACK(float, 16) : a == 8 ? BNN_PACK(float, 8) : BNN_PACK(float, 4);
-    return a == 16 ? BNN_PACK(__nv_bfloat16, 16) : a == 8 ? BNN_PACK(__nv_bfloat16, 8) : BNN_PACK(__nv_bfloat16, 4);
+    if (dt == BNN_F32) {
+        return a == 32 ? BNN_PACK(float, 32) : a == 16 ? BNN_PACK(float, 16) : a == 8 ? BNN_PACK(float, 8)
+                                                                                      : BNN_PACK(float, 4);
+    }
+    using bf16 = __nv_bfloat16;
+    return a == 32 ? BNN_PACK(bf16, 32) : a == 16 ? BNN_PACK(bf16, 16) : a == 8 ? BNN_PACK(bf16, 8) : BNN_PACK(bf16, 4);
 #undef BNN_PACK
 }
 

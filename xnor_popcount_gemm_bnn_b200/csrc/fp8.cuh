@@ -29,6 +29,14 @@ __device__ __forceinline__ uint32_t codes2(float a, float b) {
     return (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
 }
 
+// 32 bytes, read-only and not kept in L1 (one access where a row's lanes would
+// otherwise touch every 32-byte sector twice).
+__device__ __forceinline__ void ldg_stream_v8(const void* p, uint32_t* w) {
+    asm volatile("ld.global.nc.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
+                 : "l"(p));
+}
+
 // What a lane packs at a time: 16 consecutive elements as loaded (fp32, or
 // pairs of bf16), an eighth of a block.
 template <typename T>
@@ -37,11 +45,14 @@ struct Elems {
     uint32_t w[WORDS];
 
     // Elements c .. c + 15 of a row of K, 0 past K.  ALIGN: the alignment in
-    // bytes that the row's start and c * sizeof(T) share (16, 8, or less).
+    // bytes that the row's start and c * sizeof(T) share (32, 16, 8, or less).
     template <int ALIGN>
     __device__ __forceinline__ void load(const T* row, int64_t c, int64_t K) {
         if (ALIGN >= 8 && c + 16 <= K) {
-            if constexpr (ALIGN == 16) {
+            if constexpr (ALIGN == 32) {
+                #pragma unroll
+                for (int i = 0; i < WORDS; i += 8) ldg_stream_v8(reinterpret_cast<const uint32_t*>(row + c) + i, w + i);
+            } else if constexpr (ALIGN == 16) {
                 #pragma unroll
                 for (int i = 0; i < WORDS; i += 4) {
                     const uint4 q = ldg_stream_v4(reinterpret_cast<const uint32_t*>(row + c) + i);
@@ -143,24 +154,40 @@ fp8_pack_rows_kernel(const T* __restrict__ x, int64_t x_rows, int64_t K, int64_t
         Elems<T> v[U];
         #pragma unroll
         for (int u = 0; u < U; ++u) v[u].template load<ALIGN>(xr, c0 + u * 512, K);
+        // Lane u of a block's eight keeps the amax of its u-th vector, so that
+        // one division and one reciprocal serve all U.
+        float a = 0.0f;
+        bool special = false;
+        #pragma unroll
+        for (int u = 0; u < U; ++u) {
+            float m = v[u].amax();
+            special |= not_finite(m);
+            #pragma unroll
+            for (int off = 1; off < LANES; off <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+            if ((lane & (LANES - 1)) == u) a = m;
+        }
+        special = __any_sync(0xffffffffu, special);
+        if (special) {
+            #pragma unroll
+            for (int u = 0; u < U; ++u) {
+                float m = v[u].finite_amax();
+                #pragma unroll
+                for (int off = 1; off < LANES; off <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+                if ((lane & (LANES - 1)) == u) a = m;
+            }
+        }
+        const float s = block_scale(a), inv = __frcp_rn(s);
         #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int64_t c = c0 + u * 512;
-            float a = v[u].amax();
-            #pragma unroll
-            for (int off = 1; off < LANES; off <<= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, off));
-            const bool special = __any_sync(0xffffffffu, not_finite(a));
-            if (special) {
-                a = v[u].finite_amax();
-                #pragma unroll
-                for (int off = 1; off < LANES; off <<= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, off));
-            }
-            const float s = block_scale(a), inv = __frcp_rn(s);
-            if (c >= K) continue;
-            *reinterpret_cast<uint4*>(codes + r * ldc + c) =
-                special ? v[u].template codes<true>(inv) : v[u].template codes<false>(inv);
-            if ((lane & (LANES - 1)) == 0) scales[c / BLOCK * lds + r] = s;
+            const float f = __shfl_sync(0xffffffffu, inv, (lane & ~(LANES - 1)) | u);
+            if (c < K)
+                *reinterpret_cast<uint4*>(codes + r * ldc + c) =
+                    special ? v[u].template codes<true>(f) : v[u].template codes<false>(f);
         }
+        // Lane u of the eight writes the scale of the block in its u-th vector.
+        const int64_t cs = c0 - lane * 16 + (lane & ~(LANES - 1)) * 16 + (lane & (LANES - 1)) * 512;
+        if ((lane & (LANES - 1)) < U && cs < K) scales[cs / BLOCK * lds + r] = s;
     }
 }
 
