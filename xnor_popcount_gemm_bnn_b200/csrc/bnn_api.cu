@@ -1915,25 +1915,39 @@ bnn_status launch_fp8_gemm(const Fp8Operands& o, const bnn::Fp8Gemm& g, int out_
                              : launch_fp8_gemm_as<__nv_bfloat16>(o, g, stream);
 }
 
+// ALIGN: the alignment in bytes of every row's start, 32 at most.
 template <typename T, int ALIGN>
 bnn_status launch_fp8_pack(const void* x, int64_t x_rows, int64_t K, int64_t ld_x, const int32_t* row_index,
                            int64_t rows, int block_rows, uint8_t* codes, int64_t ldc, float* scales, int64_t lds,
                            cudaStream_t stream) {
+    constexpr bool wide = ALIGN >= 16;
+    constexpr int V = wide ? 1 : ALIGN / (int)sizeof(T);      // elements per load of the narrow kernels
     const T* xt = static_cast<const T*>(x);
     if (block_rows == 1) {
-        // Four (fp32: two) vectors per lane share the scale's division; when
-        // that leaves the SMs without warps, one each.
-        constexpr int U = sizeof(T) == 2 ? 4 : 2;
-        const bool many = rows * ceil_div(K, 512 * U) >= 16 * (int64_t)sm_count();
+        // Several blocks per warp share the scale's division (four vectors of
+        // four blocks, fp32 two; narrow eight blocks); when that leaves the SMs
+        // without warps, as few as possible.
+        constexpr int U = wide ? (sizeof(T) == 2 ? 4 : 2) : 8, per = wide ? 512 : bnn::fp8::BLOCK;
+        const bool many = rows * ceil_div(K, per * U) >= 16 * (int64_t)sm_count();
         const dim3 grid((unsigned)ceil_div(rows, 8),
-                        (unsigned)std::min<int64_t>(ceil_div(K, 512 * (many ? U : 1)), 65535));
-        return launch_clusters(many ? bnn::fp8_pack_rows_kernel<T, ALIGN, U> : bnn::fp8_pack_rows_kernel<T, ALIGN, 1>,
-                               grid, 256, 0, 1, stream, xt, x_rows, K, ld_x, row_index, rows, codes, ldc, scales, lds);
+                        (unsigned)std::min<int64_t>(ceil_div(K, per * (many ? U : 1)), 65535));
+        auto kernel = [&] {
+            if constexpr (wide)
+                return many ? bnn::fp8_pack_rows_kernel<T, ALIGN, U> : bnn::fp8_pack_rows_kernel<T, ALIGN, 1>;
+            else
+                return many ? bnn::fp8_pack_rows_narrow_kernel<T, V, U> : bnn::fp8_pack_rows_narrow_kernel<T, V, 1>;
+        }();
+        return launch_clusters(kernel, grid, 256, 0, 1, stream, xt, x_rows, K, ld_x, row_index, rows, codes, ldc,
+                               scales, lds);
     }
     const int64_t kblocks = ceil_div(K, bnn::fp8::BLOCK), blocks = ceil_div(rows, bnn::fp8::BLOCK) * kblocks;
     if (blocks > INT_MAX) return BNN_ERR_UNSUPPORTED;
-    return launch_clusters(bnn::fp8_pack_blocks_kernel<T, ALIGN>, dim3((unsigned)blocks), 256, 0, 1, stream, xt, rows,
-                           K, ld_x, codes, ldc, scales, lds, (unsigned)kblocks);
+    auto kernel = [&] {
+        if constexpr (wide) return bnn::fp8_pack_blocks_kernel<T, ALIGN>;
+        else return bnn::fp8_pack_blocks_narrow_kernel<T, V>;
+    }();
+    return launch_clusters(kernel, dim3((unsigned)blocks), 256, 0, 1, stream, xt, rows, K, ld_x, codes, ldc, scales,
+                           lds, (unsigned)kblocks);
 }
 
 template <typename T>
@@ -1978,7 +1992,7 @@ bnn_status bnn_fp8_pack(const void* x, bnn_dtype dt, int64_t x_rows, int64_t K, 
     if (rows == 0) return BNN_OK;
     const int64_t row_bytes = ld_x * dtype_bytes(dt);
     int a = 32;
-    while (a > 4 && !(aligned(x, (uintptr_t)a) && row_bytes % a == 0)) a >>= 1;
+    while (a > dtype_bytes(dt) && !(aligned(x, (uintptr_t)a) && row_bytes % a == 0)) a >>= 1;
     cudaStream_t s = as_cuda(stream);
 #define BNN_PACK(T, A) \
     launch_fp8_pack<T, A>(x, x_rows, K, ld_x, row_index, rows, block_rows, codes, ld_codes, scales, ld_scales, s)
@@ -1987,7 +2001,11 @@ bnn_status bnn_fp8_pack(const void* x, bnn_dtype dt, int64_t x_rows, int64_t K, 
                                                                                       : BNN_PACK(float, 4);
     }
     using bf16 = __nv_bfloat16;
-    return a == 32 ? BNN_PACK(bf16, 32) : a == 16 ? BNN_PACK(bf16, 16) : a == 8 ? BNN_PACK(bf16, 8) : BNN_PACK(bf16, 4);
+    return a == 32  ? BNN_PACK(bf16, 32)
+           : a == 16 ? BNN_PACK(bf16, 16)
+           : a == 8  ? BNN_PACK(bf16, 8)
+           : a == 4  ? BNN_PACK(bf16, 4)
+                     : BNN_PACK(bf16, 2);
 #undef BNN_PACK
 }
 

@@ -45,24 +45,18 @@ struct Elems {
     uint32_t w[WORDS];
 
     // Elements c .. c + 15 of a row of K, 0 past K.  ALIGN: the alignment in
-    // bytes that the row's start and c * sizeof(T) share (32, 16, 8, or less).
+    // bytes of every row's start (32 or 16).
     template <int ALIGN>
     __device__ __forceinline__ void load(const T* row, int64_t c, int64_t K) {
-        if (ALIGN >= 8 && c + 16 <= K) {
+        if (c + 16 <= K) {
             if constexpr (ALIGN == 32) {
                 #pragma unroll
                 for (int i = 0; i < WORDS; i += 8) ldg_stream_v8(reinterpret_cast<const uint32_t*>(row + c) + i, w + i);
-            } else if constexpr (ALIGN == 16) {
+            } else {
                 #pragma unroll
                 for (int i = 0; i < WORDS; i += 4) {
                     const uint4 q = ldg_stream_v4(reinterpret_cast<const uint32_t*>(row + c) + i);
                     w[i] = q.x; w[i + 1] = q.y; w[i + 2] = q.z; w[i + 3] = q.w;
-                }
-            } else {
-                #pragma unroll
-                for (int i = 0; i < WORDS; i += 2) {
-                    const uint2 q = __ldg(reinterpret_cast<const uint2*>(row + c) + i / 2);
-                    w[i] = q.x; w[i + 1] = q.y;
                 }
             }
         } else {
@@ -123,6 +117,90 @@ struct Elems {
         return make_uint4(o[0], o[1], o[2], o[3]);
     }
 };
+
+// Rows of a lesser alignment: a warp takes a row of a block, four elements per
+// lane in 4 / V loads of V elements (V * sizeof(T) the alignment, 8 bytes at
+// most), each load of the warp one contiguous piece.
+template <typename T, int V>
+struct Narrow {
+    float v[4];
+    static __device__ __forceinline__ int column(int i, int lane) { return (i / V) * (32 * V) + lane * V + i % V; }
+    // `n`: the columns of the block that the row has (128, less at the row's
+    // end, none past it).  Predicated loads, so that all of a lane's are in
+    // flight together; V elements that the row ends among come by rest().
+    __device__ __forceinline__ void load(const T* p, int n, int lane) {
+        #pragma unroll
+        for (int i = 0; i < 4; i += V) {
+            const int c = column(i, lane);
+            const int on = c + V <= n ? 1 : 0;
+            if constexpr (V * sizeof(T) == 8) {
+                uint32_t lo, hi;
+                asm volatile(
+                    "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %3, 0;\n\tmov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\t"
+                    "@p ld.global.nc.v2.b32 {%0, %1}, [%2];\n\t}"
+                    : "=&r"(lo), "=&r"(hi)
+                    : "l"(p + c), "r"(on));
+                if constexpr (sizeof(T) == 4) {
+                    v[i] = __uint_as_float(lo);
+                    v[i + 1] = __uint_as_float(hi);
+                } else {
+                    v[0] = __uint_as_float(lo << 16);
+                    v[1] = __uint_as_float(lo & 0xFFFF0000u);
+                    v[2] = __uint_as_float(hi << 16);
+                    v[3] = __uint_as_float(hi & 0xFFFF0000u);
+                }
+            } else if constexpr (V == 2) {
+                uint32_t q;
+                asm volatile(
+                    "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %2, 0;\n\tmov.b32 %0, 0;\n\t"
+                    "@p ld.global.nc.b32 %0, [%1];\n\t}"
+                    : "=&r"(q)
+                    : "l"(p + c), "r"(on));
+                v[i] = __uint_as_float(q << 16);
+                v[i + 1] = __uint_as_float(q & 0xFFFF0000u);
+            } else {
+                v[i] = on ? to_float(p[c]) : 0.0f;
+            }
+        }
+    }
+    __device__ __forceinline__ void rest(const T* p, int n, int lane) {
+        #pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int c = column(i, lane);
+            if (c < n && c - c % V + V > n) v[i] = to_float(p[c]);
+        }
+    }
+    __device__ __forceinline__ float amax() const {
+        return fmaxf(fmaxf(fabsf(v[0]), fabsf(v[1])), fmaxf(fabsf(v[2]), fabsf(v[3])));
+    }
+    __device__ __forceinline__ float finite_amax() const {
+        float a = 0.0f;
+        #pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (fabsf(v[i]) < __int_as_float(0x7F800000)) a = fmaxf(a, fabsf(v[i]));
+        return a;
+    }
+    // Codes to columns below `np` (n rounded up to 16) of the block's row.
+    __device__ __forceinline__ void store(uint8_t* p, int np, int lane, float inv, bool special) const {
+        float q[4];
+        #pragma unroll
+        for (int i = 0; i < 4; ++i) q[i] = special ? fmaf(v[i], 0.0f, v[i] * inv) : v[i] * inv;
+        #pragma unroll
+        for (int i = 0; i < 4; i += V) {
+            const int c = column(i, lane);
+            if (c >= np) continue;
+            if constexpr (V == 1) p[c] = (uint8_t)codes2(q[i], 0.0f);
+            else if constexpr (V == 2) *reinterpret_cast<uint16_t*>(p + c) = (uint16_t)codes2(q[i], q[i + 1]);
+            else *reinterpret_cast<uint32_t*>(p + c) = codes2(q[0], q[1]) | (codes2(q[2], q[3]) << 16);
+        }
+    }
+};
+
+// Largest of the lanes' non-negative numbers or NaN (above them all), by their
+// bits: those of magnitudes order as unsigned integers.
+__device__ __forceinline__ float warp_max_bits(float a) {
+    return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(a)));
+}
 
 // No number, or an infinity.
 __device__ __forceinline__ bool not_finite(float a) { return !(a < __int_as_float(0x7F800000)); }
@@ -191,6 +269,64 @@ fp8_pack_rows_kernel(const T* __restrict__ x, int64_t x_rows, int64_t K, int64_t
     }
 }
 
+// The same for rows of any alignment: a warp takes U blocks of one row.
+template <typename T, int V, int U>
+__global__ void __launch_bounds__(256)
+fp8_pack_rows_narrow_kernel(const T* __restrict__ x, int64_t x_rows, int64_t K, int64_t ld_x,
+                            const int32_t* __restrict__ row_index, int64_t rows, uint8_t* __restrict__ codes,
+                            int64_t ldc, float* __restrict__ scales, int64_t lds) {
+    using namespace fp8;
+    grid_dependency_wait();
+    grid_dependents_launch();
+    const int lane = threadIdx.x & 31;
+    const int64_t r = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+    if (r >= rows) return;
+    int64_t src = r;
+    if (row_index != nullptr) {
+        src = __ldg(row_index + r);
+        if (src < 0 || src >= x_rows) return;        // the row is left as it was
+    }
+    const T* xr = x + src * ld_x;
+    for (int64_t b0 = (int64_t)blockIdx.y * U; b0 * BLOCK < K; b0 += (int64_t)gridDim.y * U) {
+        Narrow<T, V> v[U];
+        #pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int64_t n = K - (b0 + u) * BLOCK;
+            v[u].load(xr + (b0 + u) * BLOCK, n < BLOCK ? (n < 0 ? 0 : (int)n) : BLOCK, lane);
+        }
+        if (V > 1 && K % V != 0) {
+            #pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int64_t n = K - (b0 + u) * BLOCK;
+                if (n > 0 && n < BLOCK) v[u].rest(xr + (b0 + u) * BLOCK, (int)n, lane);
+            }
+        }
+        float a = 0.0f;                              // lane u's: the amax of block u
+        bool special = false;
+        #pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const float m = warp_max_bits(v[u].amax());
+            special |= not_finite(m);
+            if (lane == u) a = m;
+        }
+        if (special) {
+            #pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const float m = warp_max_bits(v[u].finite_amax());
+                if (lane == u) a = m;
+            }
+        }
+        const float s = block_scale(a), inv = __frcp_rn(s);
+        #pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const float f = __shfl_sync(0xffffffffu, inv, u);
+            const int64_t n = (K + 15) / 16 * 16 - (b0 + u) * BLOCK;
+            v[u].store(codes + r * ldc + (b0 + u) * BLOCK, n < BLOCK ? (n < 0 ? 0 : (int)n) : BLOCK, lane, f, special);
+        }
+        if (lane < U && (b0 + lane) * BLOCK < K) scales[(b0 + lane) * lds + r] = s;
+    }
+}
+
 // Blocks of 128 x 128, one per CTA: 256 threads hold the block in registers
 // (64 elements each) between finding its amax and writing its codes.
 template <typename T, int ALIGN>
@@ -220,7 +356,7 @@ fp8_pack_blocks_kernel(const T* __restrict__ x, int64_t rows, int64_t K, int64_t
         #pragma unroll
         for (int u = 0; u < U; ++u) a = fmaxf(a, v[u].finite_amax());
     }
-    a = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(a)));   // magnitudes order as integers
+    a = warp_max_bits(a);
     if (lane == 0) part[warp] = a;
     __syncthreads();
     #pragma unroll
@@ -232,6 +368,51 @@ fp8_pack_blocks_kernel(const T* __restrict__ x, int64_t rows, int64_t K, int64_t
         if (r < rows && c < K)
             *reinterpret_cast<uint4*>(codes + r * ldc + c) =
                 special ? v[u].template codes<true>(inv) : v[u].template codes<false>(inv);
+    }
+    if (threadIdx.x == 0) scales[kb * lds + rb] = s;
+}
+
+// The same for rows of any alignment: a warp takes 16 rows of the block.
+template <typename T, int V>
+__global__ void __launch_bounds__(256)
+fp8_pack_blocks_narrow_kernel(const T* __restrict__ x, int64_t rows, int64_t K, int64_t ld_x,
+                              uint8_t* __restrict__ codes, int64_t ldc, float* __restrict__ scales, int64_t lds,
+                              unsigned kblocks) {
+    using namespace fp8;
+    constexpr int U = 16;
+    __shared__ float part[8];
+    grid_dependency_wait();
+    grid_dependents_launch();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t kb = blockIdx.x % kblocks, rb = blockIdx.x / kblocks;
+    const int64_t left = K - kb * BLOCK, r0 = rb * BLOCK + warp;
+    const int n = left < BLOCK ? (int)left : BLOCK;
+    Narrow<T, V> v[U];
+    #pragma unroll
+    for (int u = 0; u < U; ++u) v[u].load(x + min(r0 + 8 * u, rows - 1) * ld_x + kb * BLOCK, n, lane);
+    if (V > 1 && n % V != 0) {
+        #pragma unroll
+        for (int u = 0; u < U; ++u) v[u].rest(x + min(r0 + 8 * u, rows - 1) * ld_x + kb * BLOCK, n, lane);
+    }
+    float a = v[0].amax();
+    #pragma unroll
+    for (int u = 1; u < U; ++u) a = fmaxf(a, v[u].amax());
+    const bool special = __syncthreads_or(not_finite(a));
+    if (special) {
+        a = 0.0f;
+        #pragma unroll
+        for (int u = 0; u < U; ++u) a = fmaxf(a, v[u].finite_amax());
+    }
+    a = warp_max_bits(a);
+    if (lane == 0) part[warp] = a;
+    __syncthreads();
+    #pragma unroll
+    for (int w = 0; w < 8; ++w) a = fmaxf(a, part[w]);
+    const float s = block_scale(a), inv = __frcp_rn(s);
+    #pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const int64_t r = r0 + 8 * u;
+        if (r < rows) v[u].store(codes + r * ldc + kb * BLOCK, (n + 15) / 16 * 16, lane, inv, special);
     }
     if (threadIdx.x == 0) scales[kb * lds + rb] = s;
 }
