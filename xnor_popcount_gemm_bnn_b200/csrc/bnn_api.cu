@@ -1961,11 +1961,20 @@ void launch_route_topk(const void* logits, const bnn::RouteParams& p, cudaStream
 }
 
 template <typename T, typename O>
-void launch_route_combine(const void* Y, int64_t R, int64_t N, int64_t ldy, const int32_t* slot_row,
-                          const float* weights, int64_t T_, int64_t k, void* out, int64_t ldo, cudaStream_t stream) {
-    const dim3 grid((unsigned)T_, (unsigned)ceil_div(N, 256));
-    bnn::route_combine_kernel<T, O><<<grid, 256, 0, stream>>>(static_cast<const T*>(Y), R, N, ldy, slot_row, weights,
-                                                             (int)k, static_cast<O*>(out), ldo);
+bnn_status launch_route_combine(const void* Y, int64_t R, int64_t N, int64_t ldy, const int32_t* slot_row,
+                                const float* weights, int64_t tokens, int64_t k, void* out, int64_t ldo,
+                                cudaStream_t stream) {
+    constexpr int V = 16 / (int)sizeof(T);
+    // Whole vectors in every row of Y and out; N itself a multiple of V.
+    const bool vec = aligned(Y, 16) && ldy % V == 0 && N % V == 0 && aligned(out, 8) && ldo * (int64_t)sizeof(O) % 8 == 0;
+    auto run = [&](auto kernel, int64_t per) {
+        const dim3 grid((unsigned)tokens, (unsigned)std::min<int64_t>(ceil_div(N, per), 65535));
+        return launch_clusters(kernel, grid, bnn::kCombineThreads, 0, 1, stream, static_cast<const T*>(Y), R, N, ldy,
+                               slot_row, weights, (int)k, static_cast<O*>(out), ldo);
+    };
+    constexpr int64_t threads = bnn::kCombineThreads;
+    if (vec) return run(bnn::route_combine_kernel<T, O, V, 1>, threads * V);
+    return run(bnn::route_combine_kernel<T, O, 1, 4>, threads * 4);
 }
 
 }  // namespace
@@ -2104,15 +2113,10 @@ bnn_status bnn_route_combine(const void* Y, bnn_dtype dt, int64_t R, int64_t N, 
     if (T == 0 || N == 0) return BNN_OK;
     cudaStream_t s = as_cuda(stream);
     using bf16 = __nv_bfloat16;
-    if (dt == BNN_F32 && out_dt == BNN_F32)
-        launch_route_combine<float, float>(Y, R, N, ld_y, slot_row, weights, T, k, out, ld_out, s);
-    else if (dt == BNN_F32)
-        launch_route_combine<float, bf16>(Y, R, N, ld_y, slot_row, weights, T, k, out, ld_out, s);
-    else if (out_dt == BNN_F32)
-        launch_route_combine<bf16, float>(Y, R, N, ld_y, slot_row, weights, T, k, out, ld_out, s);
-    else
-        launch_route_combine<bf16, bf16>(Y, R, N, ld_y, slot_row, weights, T, k, out, ld_out, s);
-    return launch_status();
+    auto go = [&](auto launch) { return launch(Y, R, N, ld_y, slot_row, weights, T, k, out, ld_out, s); };
+    if (dt == BNN_F32)
+        return out_dt == BNN_F32 ? go(launch_route_combine<float, float>) : go(launch_route_combine<float, bf16>);
+    return out_dt == BNN_F32 ? go(launch_route_combine<bf16, float>) : go(launch_route_combine<bf16, bf16>);
 }
 
 }  // extern "C"

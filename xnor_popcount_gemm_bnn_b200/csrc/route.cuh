@@ -285,6 +285,9 @@ route_plan_kernel(const int32_t* __restrict__ idx, int slots, int k, int E, int3
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
+// ---------------------------------------------------------------------------
+// out[t, n] = sum_j weights[t, j] * Y[slot_row[t, j], n], in j order, fp32.
+// ---------------------------------------------------------------------------
 template <typename T>
 __device__ __forceinline__ T route_out(float v);
 template <>
@@ -292,20 +295,124 @@ __device__ __forceinline__ float route_out<float>(float v) { return v; }
 template <>
 __device__ __forceinline__ __nv_bfloat16 route_out<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
 
-// out[t, n] = sum_j weights[t, j] * Y[slot_row[t, j], n], in j order, fp32.
-template <typename T, typename O>
-__global__ void __launch_bounds__(256)
+// 16 bytes, read-only and not kept in L1; zeros where `on` is 0.
+__device__ __forceinline__ uint4 ldg_stream_v4_if(const void* p, int on) {
+    uint4 v;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %5, 0;\n\t"
+        "mov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\tmov.b32 %2, 0;\n\tmov.b32 %3, 0;\n\t"
+        "@p ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];\n\t}"
+        : "=&r"(v.x), "=&r"(v.y), "=&r"(v.z), "=&r"(v.w)
+        : "l"(p), "r"(on));
+    return v;
+}
+
+__device__ __forceinline__ float ldg_if(const float* p, int on) {
+    float v;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %2, 0;\n\tmov.b32 %0, 0;\n\t@p ld.global.nc.f32 %0, [%1];\n\t}"
+        : "=&f"(v)
+        : "l"(p), "r"(on));
+    return v;
+}
+__device__ __forceinline__ float ldg_if(const __nv_bfloat16* p, int on) {
+    unsigned short v;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %2, 0;\n\tmov.b16 %0, 0;\n\t@p ld.global.nc.u16 %0, [%1];\n\t}"
+        : "=&h"(v)
+        : "l"(p), "r"(on));
+    return __uint_as_float((uint32_t)v << 16);
+}
+
+// Bound by reading the k rows of a token, each once.  A block takes one token
+// and C pieces of V elements per thread, THREADS * V apart; the lanes hold the
+// token's rows and weights, and the loads of eight rows are in flight
+// together (predicated: a branch would wait for each).  V = 16 bytes of T
+// where every row of Y and out allows it, else 1.
+constexpr int kCombineThreads = 128;
+template <typename T, typename O, int V, int C>
+__global__ void __launch_bounds__(kCombineThreads)
 route_combine_kernel(const T* __restrict__ Y, int64_t R, int64_t N, int64_t ldy, const int32_t* __restrict__ slot_row,
                      const float* __restrict__ weights, int k, O* __restrict__ out, int64_t ldo) {
+    grid_dependency_wait();
+    grid_dependents_launch();
+    const int lane = threadIdx.x & 31;
+    static_assert(V == 1 || C == 1, "one vector per thread");
     const int64_t t = blockIdx.x;
-    const int64_t n = (int64_t)blockIdx.y * blockDim.x + threadIdx.x;
-    if (n >= N) return;
-    float y = 0.0f;
-    for (int j = 0; j < k; ++j) {
-        const int64_t r = slot_row[t * k + j];
-        if (r >= 0 && r < R) y = fmaf(weights[t * k + j], to_float(Y[r * ldy + n]), y);
+    constexpr int PER = kCombineThreads * C * V;
+    for (int64_t base = (int64_t)blockIdx.y * PER; base < N; base += (int64_t)gridDim.y * PER) {
+        const int64_t n0 = base + threadIdx.x * V;
+        float y[C][V];
+        #pragma unroll
+        for (int c = 0; c < C; ++c) {
+            #pragma unroll
+            for (int i = 0; i < V; ++i) y[c][i] = 0.0f;
+        }
+        for (int j0 = 0; j0 < k; j0 += 32) {
+            int row = -1;
+            float w = 0.0f;
+            if (j0 + lane < k) {
+                row = __ldg(slot_row + t * k + j0 + lane);
+                w = __ldg(weights + t * k + j0 + lane);
+            }
+            const int n_j = min(32, k - j0);
+            constexpr int J = V == 1 ? 4 : 8;
+            for (int j = 0; j < n_j; j += J) {
+                // Slots past k hold row -1 and weight 0.
+                uint4 q[V == 1 ? 1 : J];
+                float s[V == 1 ? J : 1][C], f[J];
+                #pragma unroll
+                for (int i = 0; i < J; ++i) {
+                    const int64_t r = __shfl_sync(0xffffffffu, row, j + i);
+                    const bool on = r >= 0 && r < R;
+                    f[i] = __shfl_sync(0xffffffffu, w, j + i);
+                    f[i] = on ? f[i] : 0.0f;
+                    #pragma unroll
+                    for (int c = 0; c < C; ++c) {
+                        const int64_t n = n0 + c * (kCombineThreads * V);
+                        if constexpr (V == 1) s[i][c] = ldg_if(Y + r * ldy + n, on && n < N ? 1 : 0);
+                        else q[i] = ldg_stream_v4_if(Y + r * ldy + n, on && n < N ? 1 : 0);
+                    }
+                }
+                #pragma unroll
+                for (int i = 0; i < J; ++i) {
+                    #pragma unroll
+                    for (int c = 0; c < C; ++c) {
+                        if constexpr (V == 1) {
+                            y[c][0] = fmaf(f[i], s[i][c], y[c][0]);
+                        } else {
+                            const uint32_t u[4] = {q[i].x, q[i].y, q[i].z, q[i].w};
+                            #pragma unroll
+                            for (int e = 0; e < V; ++e) {
+                                float v;
+                                if constexpr (sizeof(T) == 4) v = __uint_as_float(u[e]);
+                                else v = __uint_as_float((e & 1) ? (u[e >> 1] & 0xFFFF0000u) : (u[e >> 1] << 16));
+                                y[c][e] = fmaf(f[i], v, y[c][e]);
+                            }
+                        }
+                    }
+                }
+            }
+        }
+        #pragma unroll
+        for (int c = 0; c < C; ++c) {
+            const int64_t n = n0 + (int64_t)c * (kCombineThreads * V);
+            if (n >= N) continue;
+            O* o = out + t * ldo + n;
+            if constexpr (V == 1) {
+                o[0] = route_out<O>(y[c][0]);
+            } else {
+                union {
+                    O e[V];
+                    uint2 w[V * sizeof(O) / 8];
+                } q;
+                #pragma unroll
+                for (int i = 0; i < V; ++i) q.e[i] = route_out<O>(y[c][i]);
+                #pragma unroll
+                for (int i = 0; i < (int)(V * sizeof(O) / 8); ++i) reinterpret_cast<uint2*>(o)[i] = q.w[i];
+            }
+        }
     }
-    out[t * ldo + n] = route_out<O>(y);
 }
 
 }  // namespace bnn
