@@ -1950,14 +1950,59 @@ bnn_status launch_fp8_pack(const void* x, int64_t x_rows, int64_t K, int64_t ld_
                            lds, (unsigned)kblocks);
 }
 
-template <typename T>
-void launch_route_topk(const void* logits, const bnn::RouteParams& p, cudaStream_t stream) {
+struct RoutePlan {
+    int32_t *offsets, *row_token, *slot_row;
+};
+
+// Per-device one-time opt-in of the plan kernels to their shared memory.
+template <typename T, int NI>
+bool route_small_opt_in() {
+    return cudaFuncSetAttribute(bnn::route_small_kernel<T, NI>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                bnn::route_plan_smem(32 * NI)) == cudaSuccess;
+}
+bool route_smem_configured() {
+    constexpr int kMaxDevices = 64;
+    static std::atomic<int> done[kMaxDevices];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0) return false;
+    if (dev < kMaxDevices && done[dev].load(std::memory_order_acquire)) return true;
+    using bf16 = __nv_bfloat16;
+    if (cudaFuncSetAttribute(bnn::route_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             bnn::route_plan_smem(bnn::route::MAX_E)) != cudaSuccess ||
+        !route_small_opt_in<float, 2>() || !route_small_opt_in<float, 4>() || !route_small_opt_in<float, 8>() ||
+        !route_small_opt_in<float, 16>() || !route_small_opt_in<bf16, 2>() || !route_small_opt_in<bf16, 4>() ||
+        !route_small_opt_in<bf16, 8>() || !route_small_opt_in<bf16, 16>())
+        return false;
+    if (dev < kMaxDevices) done[dev].store(1, std::memory_order_release);
+    return true;
+}
+
+template <typename T, int NI>
+bnn_status launch_route_as(const void* logits, const bnn::RouteParams& params, const RoutePlan& plan,
+                           cudaStream_t stream) {
+    using namespace bnn::route;
     const T* l = static_cast<const T*>(logits);
-    const unsigned grid = (unsigned)ceil_div(p.T, 8);
-    if (p.E <= 64) bnn::route_topk_kernel<T, 2><<<grid, 256, 0, stream>>>(l, p);
-    else if (p.E <= 128) bnn::route_topk_kernel<T, 4><<<grid, 256, 0, stream>>>(l, p);
-    else if (p.E <= 256) bnn::route_topk_kernel<T, 8><<<grid, 256, 0, stream>>>(l, p);
-    else bnn::route_topk_kernel<T, 16><<<grid, 256, 0, stream>>>(l, p);
+    constexpr int VB = NI * (int)sizeof(T) < 16 ? NI * (int)sizeof(T) : 16;
+    bnn::RouteParams p = params;
+    p.vec = aligned(l, VB) && p.ld * (int64_t)sizeof(T) % VB == 0 && p.E * (int64_t)sizeof(T) % VB == 0 ? 1 : 0;
+    // Few tokens with a plan: both in one CTA (a second launch costs more
+    // than the SMs it leaves idle).
+    if (plan.offsets != nullptr && p.T <= SMALL_T)
+        return launch_clusters(bnn::route_small_kernel<T, NI>, dim3(1), PLAN_THREADS, bnn::route_plan_smem(p.E), 1,
+                               stream, l, p, plan.offsets, plan.row_token, plan.slot_row);
+    const bnn_status st =
+        launch_clusters(bnn::route_topk_kernel<T, NI>, dim3((unsigned)ceil_div(p.T, 8)), 256, 0, 1, stream, l, p);
+    if (st != BNN_OK || plan.offsets == nullptr) return st;
+    return launch_clusters(bnn::route_plan_kernel, dim3(PLAN_CLUSTER), PLAN_THREADS, bnn::route_plan_smem(p.E),
+                           PLAN_CLUSTER, stream, (const int32_t*)p.idx, p.T * p.k, p.k, p.E, plan.offsets,
+                           plan.row_token, plan.slot_row);
+}
+template <typename T>
+bnn_status launch_route(const void* logits, const bnn::RouteParams& p, const RoutePlan& plan, cudaStream_t stream) {
+    if (p.E <= 64) return launch_route_as<T, 2>(logits, p, plan, stream);
+    if (p.E <= 128) return launch_route_as<T, 4>(logits, p, plan, stream);
+    if (p.E <= 256) return launch_route_as<T, 8>(logits, p, plan, stream);
+    return launch_route_as<T, 16>(logits, p, plan, stream);
 }
 
 template <typename T, typename O>
@@ -2066,36 +2111,15 @@ bnn_status bnn_route(const void* logits, bnn_dtype dt, int64_t T, int64_t E, int
     if (!aligned(logits, (uintptr_t)dtype_bytes(dt)) || !aligned(idx, 4) || !aligned(weights, 4) ||
         !aligned(offsets, 4) || !aligned(row_token, 4) || !aligned(slot_row, 4) || !aligned(rp->bias, 4))
         return BNN_ERR_ALIGNMENT;
-    cudaStream_t s = as_cuda(stream);
-    if (T > 0) {
-        const bnn::RouteParams p{(int)T,        (int)E,           rp->k,         ld,
-                                 rp->score,     rp->n_groups,     rp->kept_groups, rp->group_top,
-                                 rp->renormalize, rp->scale,      rp->bias,      idx,
-                                 weights};
-        if (dt == BNN_F32) launch_route_topk<float>(logits, p, s);
-        else launch_route_topk<__nv_bfloat16>(logits, p, s);
-        const bnn_status st = launch_status();
-        if (st != BNN_OK) return st;
-    }
-    if (!plan) return BNN_OK;
-    cudaLaunchConfig_t cfg{};
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = PLAN_CLUSTER;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    cfg.gridDim = dim3(PLAN_CLUSTER);
-    cfg.blockDim = dim3(PLAN_THREADS);
-    cfg.dynamicSmemBytes = (size_t)(2 * MAX_E + PLAN_THREADS / 32 * E) * 4;
-    cfg.stream = s;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, bnn::route_plan_kernel, (const int32_t*)idx, (int)(T * rp->k), (int)rp->k, (int)E,
-                           offsets, row_token, slot_row) != cudaSuccess) {
-        (void)cudaGetLastError();
-        return BNN_ERR_CUDA;
-    }
-    return launch_status();
+    if (T == 0 && !plan) return BNN_OK;
+    if (!route_smem_configured()) return BNN_ERR_CUDA;
+    // No tokens with a plan: the small kernel writes zero offsets.
+    const bnn::RouteParams p{(int)T,          (int)E,    rp->k,    ld,  rp->score,
+                             rp->n_groups,    rp->kept_groups, rp->group_top, rp->renormalize, rp->scale,
+                             rp->bias,        idx,       weights,   0};
+    const RoutePlan rows{offsets, row_token, slot_row};
+    return dt == BNN_F32 ? launch_route<float>(logits, p, rows, as_cuda(stream))
+                         : launch_route<__nv_bfloat16>(logits, p, rows, as_cuda(stream));
 }
 
 bnn_status bnn_route_combine(const void* Y, bnn_dtype dt, int64_t R, int64_t N, int64_t ld_y, const int32_t* slot_row,

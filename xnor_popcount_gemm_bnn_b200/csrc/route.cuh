@@ -12,7 +12,9 @@ constexpr int MAX_E = 512;
 constexpr int MAX_K = 16;
 constexpr int MAX_GROUPS = 32;
 constexpr int PLAN_CLUSTER = 8;
-constexpr int PLAN_THREADS = 512;
+constexpr int PLAN_THREADS = 1024;
+constexpr int PLAN_WARPS = PLAN_THREADS / 32;
+constexpr int SMALL_T = 16;                  // tokens that one CTA chooses for and plans in one launch
 }  // namespace route
 
 struct RouteParams {
@@ -23,13 +25,20 @@ struct RouteParams {
     const float* bias;
     int32_t* idx;
     float* weights;
+    int vec;                                     // rows of logits can be read in vectors
 };
 
+// ---------------------------------------------------------------------------
+// The choice in fp64: what the result is defined by.
+// ---------------------------------------------------------------------------
 // Doubles as unsigned keys in the same order (negative ones reversed); 0 is
 // below every number's key and marks what cannot be chosen.
 __device__ __forceinline__ unsigned long long order_key(double v) {
     const unsigned long long b = (unsigned long long)__double_as_longlong(v + 0.0);   // -0 -> +0
     return (b >> 63) ? ~b : b | 0x8000000000000000ull;
+}
+__device__ __forceinline__ double key_value(unsigned long long q) {
+    return __longlong_as_double((long long)((q >> 63) ? q & 0x7FFFFFFFFFFFFFFFull : ~q));
 }
 
 // Largest key of the warp and the lowest index that has it.
@@ -52,36 +61,64 @@ __device__ __forceinline__ double warp_sum(double v) {
     return v;
 }
 
-// One warp per token; lane l holds experts l, l + 32, ...  Scores and the
-// choice in fp64: neighbouring scores of a few hundred experts are often
-// closer than fp32 tells apart, and the chosen set is a whole-number result.
-template <typename T, int NI>
-__global__ void __launch_bounds__(256) route_topk_kernel(const T* __restrict__ logits, RouteParams p) {
-    using namespace route;
-    const int lane = threadIdx.x & 31;
-    const int t = blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
-    if (t >= p.T) return;
-    const T* row = logits + (int64_t)t * p.ld;
+// NaN masks an expert as -inf does; +inf counts as the largest finite number.
+__device__ __forceinline__ float logit_of(float l) {
+    return l > -CUDART_INF_F ? fminf(l, 3.402823466e38f) : -CUDART_INF_F;
+}
+
+// Logits lane * NI .. lane * NI + NI - 1 of a row, -inf past E and where
+// masked (-inf or NaN), +inf as the largest finite number; in vectors of up to
+// 16 bytes where p.vec says that rows and E allow them.
+template <int NI, typename T>
+__device__ __forceinline__ void load_logits(const T* __restrict__ row, const RouteParams& p, int lane, float (&l)[NI]) {
+    constexpr int VE = NI * (int)sizeof(T) < 16 ? NI : 16 / (int)sizeof(T);
+    if (p.vec) {
+        #pragma unroll
+        for (int i = 0; i < NI; i += VE) {
+            union {
+                T e[VE];
+                uint32_t w[VE * sizeof(T) / 4];
+            } q;
+            const int e = lane * NI + i;
+            if (e < p.E) {
+                if constexpr (VE * sizeof(T) == 16) {
+                    const uint4 v = __ldg(reinterpret_cast<const uint4*>(row + e));
+                    q.w[0] = v.x; q.w[1] = v.y; q.w[2] = v.z; q.w[3] = v.w;
+                } else if constexpr (VE * sizeof(T) == 8) {
+                    const uint2 v = __ldg(reinterpret_cast<const uint2*>(row + e));
+                    q.w[0] = v.x; q.w[1] = v.y;
+                } else {
+                    q.w[0] = __ldg(reinterpret_cast<const uint32_t*>(row + e));
+                }
+            }
+            #pragma unroll
+            for (int j = 0; j < VE; ++j) l[i + j] = e < p.E ? to_float(q.e[j]) : -CUDART_INF_F;
+        }
+    } else {
+        #pragma unroll
+        for (int i = 0; i < NI; ++i) l[i] = lane * NI + i < p.E ? to_float(row[lane * NI + i]) : -CUDART_INF_F;
+    }
+    #pragma unroll
+    for (int i = 0; i < NI; ++i) l[i] = logit_of(l[i]);
+}
+
+// One warp, one token.  Lane j < k gets the j-th expert (-1: none) and its weight.
+template <int NI, typename T>
+__device__ __noinline__ void route_exact(const T* __restrict__ row, const RouteParams& p, int lane, int& my_e,
+                                         float& my_w) {
+    float l[NI];
+    load_logits<NI>(row, p, lane, l);
     double score[NI];
     unsigned long long key[NI];
     double top = -CUDART_INF;
     #pragma unroll
-    for (int i = 0; i < NI; ++i) {
-        const int e = lane + 32 * i;
-        float l = e < p.E ? to_float(row[e]) : -CUDART_INF_F;
-        if (!(l > -CUDART_INF_F)) l = -CUDART_INF_F;          // NaN masks an expert as -inf does
-        if (l == CUDART_INF_F) l = 3.402823466e38f;
-        score[i] = (double)l;
-        top = fmax(top, score[i]);
-    }
+    for (int i = 0; i < NI; ++i) top = fmax(top, (double)l[i]);
     if (!p.sigmoid) {
         top = warp_max(top);
         double sum = 0.0;
         #pragma unroll
         for (int i = 0; i < NI; ++i) {
-            const bool on = score[i] > -CUDART_INF;
-            key[i] = on ? 1ull : 0ull;
-            score[i] = on ? exp(score[i] - top) : 0.0;
+            score[i] = l[i] > -CUDART_INF_F ? exp((double)l[i] - top) : 0.0;
             sum += score[i];
         }
         sum = warp_sum(sum);
@@ -89,21 +126,17 @@ __global__ void __launch_bounds__(256) route_topk_kernel(const T* __restrict__ l
         for (int i = 0; i < NI; ++i) score[i] = sum > 0.0 ? score[i] / sum : 0.0;
     } else {
         #pragma unroll
-        for (int i = 0; i < NI; ++i) {
-            const bool on = score[i] > -CUDART_INF;
-            key[i] = on ? 1ull : 0ull;
-            score[i] = on ? 1.0 / (1.0 + exp(-score[i])) : 0.0;
-        }
+        for (int i = 0; i < NI; ++i) score[i] = l[i] > -CUDART_INF_F ? 1.0 / (1.0 + exp(-(double)l[i])) : 0.0;
     }
     #pragma unroll
     for (int i = 0; i < NI; ++i) {
-        const int e = lane + 32 * i;
-        if (key[i] == 0) continue;
-        double c = score[i];
-        if (p.bias != nullptr) c += (double)__ldg(p.bias + e);
+        const int e = lane * NI + i;
+        key[i] = 0ull;
+        if (!(l[i] > -CUDART_INF_F)) continue;
+        const double c = score[i] + (p.bias != nullptr ? (double)__ldg(p.bias + e) : 0.0);
         key[i] = c > -CUDART_INF ? order_key(c) : 0ull;       // a NaN or -inf bias masks too
     }
-    if (p.groups > 1 && p.kept < p.groups) {
+    if (p.kept < p.groups) {
         // Lane g keeps group g's score: its largest choice value, or the sum
         // of its two largest.
         const int per = p.E / p.groups;
@@ -112,7 +145,7 @@ __global__ void __launch_bounds__(256) route_topk_kernel(const T* __restrict__ l
             unsigned long long k1 = 0, k2 = 0;
             #pragma unroll
             for (int i = 0; i < NI; ++i) {
-                const int e = lane + 32 * i;
+                const int e = lane * NI + i;
                 if (e / per == g && e < p.E) {
                     if (key[i] > k1) { k2 = k1; k1 = key[i]; }
                     else if (key[i] > k2) k2 = key[i];
@@ -125,14 +158,8 @@ __global__ void __launch_bounds__(256) route_topk_kernel(const T* __restrict__ l
                 if (o1 > k1) { k2 = max(k1, o2); k1 = o1; }
                 else k2 = max(k2, o1);
             }
-            unsigned long long gk = k1;
-            if (p.group_top > 1 && k2 != 0) {
-                auto val = [](unsigned long long q) {
-                    return __longlong_as_double((long long)((q >> 63) ? q & 0x7FFFFFFFFFFFFFFFull : ~q));
-                };
-                gk = order_key(val(k1) + val(k2));
-            }
-            if (lane == g) mine = gk;
+            if (p.group_top > 1 && k2 != 0) k1 = order_key(key_value(k1) + key_value(k2));
+            if (lane == g) mine = k1;
         }
         unsigned kept = 0;
         for (int j = 0; j < p.kept; ++j) {
@@ -145,12 +172,12 @@ __global__ void __launch_bounds__(256) route_topk_kernel(const T* __restrict__ l
         }
         #pragma unroll
         for (int i = 0; i < NI; ++i) {
-            const int e = lane + 32 * i;
+            const int e = lane * NI + i;
             if (e < p.E && ((kept >> (e / per)) & 1u) == 0) key[i] = 0;
         }
     }
     // k rounds: every lane offers its best, the winner's lane gives it up.
-    int my_e = -1;
+    my_e = -1;
     double my_s = 0.0;
     for (int j = 0; j < p.k; ++j) {
         unsigned long long b = 0;
@@ -158,92 +185,320 @@ __global__ void __launch_bounds__(256) route_topk_kernel(const T* __restrict__ l
         double s = 0.0;
         #pragma unroll
         for (int i = 0; i < NI; ++i)
-            if (key[i] > b) { b = key[i]; id = lane + 32 * i; s = score[i]; }
+            if (key[i] > b) { b = key[i]; id = lane * NI + i; s = score[i]; }
         int win = id;
         warp_best(b, win);
         if (b == 0) break;
-        const double ws = __shfl_sync(0xffffffffu, s, win & 31);
+        const double ws = __shfl_sync(0xffffffffu, s, win / NI);
         if (lane == j) { my_e = win; my_s = ws; }
-        if (lane == (win & 31)) {
-            #pragma unroll
-            for (int i = 0; i < NI; ++i)
-                if (lane + 32 * i == win) key[i] = 0;
-        }
+        #pragma unroll
+        for (int i = 0; i < NI; ++i)
+            if (lane * NI + i == win) key[i] = 0;
     }
     const double sum = warp_sum(my_s);
+    my_w = (float)((p.renorm ? (sum > 0.0 ? my_s / sum : 0.0) : my_s) * p.scale);
+}
+
+// ---------------------------------------------------------------------------
+// The choice in fp32, where it is certain.
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ uint32_t order_key(float v) {
+    const uint32_t b = __float_as_uint(v + 0.0f);
+    return (b >> 31) ? ~b : b | 0x80000000u;
+}
+__device__ __forceinline__ float key_value(uint32_t q) {
+    return __uint_as_float((q >> 31) ? q & 0x7FFFFFFFu : ~q);
+}
+
+// One warp, one token, lane l holding experts l * NI .. l * NI + NI - 1 (the
+// lowest index of equal keys is then the first of the lowest lane).  Scores
+// are taken in fp32 and every decision is checked against their errors.
+// Choice values nearer than that (other than the same logit and bias, a tie in
+// any precision) are compared again in fp64, one candidate per lane; what that
+// does not settle -- groups on the border, a softmax with a bias, scores that
+// underflow -- goes to route_exact().  In fp64 throughout, the exponentials
+// alone would take several times the kernel's time.
+//   Errors: expf 2^-22 relative (2 ulp), the approximate quotient as much, sums
+//   2^-24 each.  Sigmoid: at most 2^-20.6 of the score; softmax: 2^-19 +
+//   |l - max| 2^-24 of it (21 additions for 512 experts), taken for up to 30
+//   below the maximum; the bias' addition 2^-24 of the choice value.
+template <int NI, typename T>
+__device__ __forceinline__ void route_token(const T* __restrict__ row, const RouteParams& p, int lane, int& my_e,
+                                            float& my_w) {
+    uint32_t key[NI];
+    float top = -CUDART_INF_F, inv = 0.0f, big = 0.0f;         // big: largest |choice value| or score
+    const float rel = p.sigmoid ? 6.3e-7f : 4.0e-6f;
+    {
+        float s[NI];
+        load_logits<NI>(row, p, lane, s);
+        uint32_t on = 0;                                       // experts that are not masked
+        #pragma unroll
+        for (int i = 0; i < NI; ++i) {
+            on |= (s[i] > -CUDART_INF_F ? 1u : 0u) << i;
+            top = fmaxf(top, s[i]);
+        }
+        if (!p.sigmoid) {
+            #pragma unroll
+            for (int off = 16; off >= 1; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+            float sum = 0.0f;
+            #pragma unroll
+            for (int i = 0; i < NI; ++i) {
+                s[i] = (on >> i) & 1u ? expf(s[i] - top) : 0.0f;
+                sum += s[i];
+            }
+            #pragma unroll
+            for (int off = 16; off >= 1; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+            inv = sum > 0.0f ? __fdividef(1.0f, sum) : 0.0f;
+            #pragma unroll
+            for (int i = 0; i < NI; ++i) s[i] *= inv;
+        } else {
+            #pragma unroll
+            for (int i = 0; i < NI; ++i) s[i] = __fdividef(1.0f, 1.0f + expf(-s[i]));
+        }
+        #pragma unroll
+        for (int i = 0; i < NI; ++i) {
+            const int e = lane * NI + i;
+            const float c = p.bias != nullptr && e < p.E ? s[i] + __ldg(p.bias + e) : s[i];
+            const bool ok = ((on >> i) & 1u) && c > -CUDART_INF_F;
+            key[i] = ok ? order_key(c) : 0u;
+            if (ok) big = fmaxf(big, fmaxf(s[i], fabsf(c)));
+        }
+    }
+    bool sure = true;
+    float slack = 0.0f;                                        // two errors of any choice value
+    if (p.bias != nullptr || p.kept < p.groups) {
+        big = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(big)));
+        slack = 2.0f * (rel + 1.2e-7f) * big;
+        sure = big < 1e30f;
+    }
+    if (p.kept < p.groups) {
+        const int per = p.E / p.groups;
+        uint32_t mine = 0;                                     // lane g: group g's score
+        if (per % NI == 0 && ((per / NI) & (per / NI - 1)) == 0) {
+            // Groups of whole lanes, a power of two of them.
+            uint32_t k1 = 0, k2 = 0;
+            #pragma unroll
+            for (int i = 0; i < NI; ++i) {
+                k2 = max(k2, min(k1, key[i]));
+                k1 = max(k1, key[i]);
+            }
+            const int lanes = per / NI;
+            for (int off = 1; off < lanes; off <<= 1) {
+                const uint32_t o1 = __shfl_xor_sync(0xffffffffu, k1, off), o2 = __shfl_xor_sync(0xffffffffu, k2, off);
+                k2 = max(max(k2, o2), min(k1, o1));
+                k1 = max(k1, o1);
+            }
+            if (p.group_top > 1 && k2 != 0) k1 = order_key(key_value(k1) + key_value(k2));
+            mine = __shfl_sync(0xffffffffu, k1, (lane * lanes) & 31);
+        } else {
+            for (int g = 0; g < p.groups; ++g) {
+                uint32_t k1 = 0, k2 = 0;
+                #pragma unroll
+                for (int i = 0; i < NI; ++i) {
+                    const uint32_t q = (lane * NI + i) / per == g ? key[i] : 0u;
+                    k2 = max(k2, min(k1, q));
+                    k1 = max(k1, q);
+                }
+                const uint32_t t1 = __reduce_max_sync(0xffffffffu, k1);
+                // The second: the winner's lane (one of them) offers its other.
+                const unsigned has = __ballot_sync(0xffffffffu, k1 == t1);
+                const uint32_t t2 = __reduce_max_sync(0xffffffffu, lane == __ffs(has) - 1 ? k2 : k1);
+                uint32_t q = t1;
+                if (p.group_top > 1 && t2 != 0) q = order_key(key_value(t1) + key_value(t2));
+                if (lane == g) mine = q;
+            }
+        }
+        if (lane >= p.groups) mine = 0;
+        int rank = 0;
+        for (int g = 0; g < p.groups; ++g) {
+            const uint32_t o = __shfl_sync(0xffffffffu, mine, g);
+            rank += (o > mine || (o == mine && g < lane)) ? 1 : 0;
+        }
+        const bool in = mine != 0 && rank < p.kept;
+        const uint32_t least = __reduce_min_sync(0xffffffffu, in ? mine : 0xFFFFFFFFu);
+        const uint32_t next = __reduce_max_sync(0xffffffffu, in ? 0u : mine);
+        if (next != 0) sure = sure && key_value(least) - key_value(next) > 2.0f * slack;
+        const unsigned kept = __ballot_sync(0xffffffffu, in);
+        #pragma unroll
+        for (int i = 0; i < NI; ++i) {
+            const int e = lane * NI + i;
+            if (e < p.E && ((kept >> (e / per)) & 1u) == 0) key[i] = 0;
+        }
+    }
+    // Candidates in order, the j-th to lane j: k of them, and on to the first
+    // that is certainly below.  Every lane offers its best, the winner's lane
+    // gives it up.  Without a bias the order is that of the scores, whose errors
+    // are relative: no score below has a larger one.
+    const float step = 2.0f * rel;
+    int cand = -1, m = 0;
+    float my_c = 0.0f, last = 0.0f;
+    for (; m < 32; ++m) {
+        uint32_t b = 0;
+        int at = 0;
+        #pragma unroll
+        for (int i = 0; i < NI; ++i)
+            if (key[i] > b) { b = key[i]; at = i; }
+        const uint32_t best = __reduce_max_sync(0xffffffffu, b);
+        if (best == 0) break;
+        const float c = key_value(best);
+        if (m >= p.k && last - c > (p.bias != nullptr ? slack : step * last)) break;
+        last = c;
+        const int from = __ffs(__ballot_sync(0xffffffffu, b == best)) - 1;
+        const int win = from * NI + __shfl_sync(0xffffffffu, at, from);
+        if (lane == m) { cand = win; my_c = c; }
+        #pragma unroll
+        for (int i = 0; i < NI; ++i)
+            if (lane * NI + i == win) key[i] = 0;
+    }
+    sure = sure && (m < 32 || p.E <= 32);
+    float l = 0.0f, bias = 0.0f;
+    if (cand >= 0) {
+        l = logit_of(to_float(row[cand]));
+        if (p.bias != nullptr) bias = __ldg(p.bias + cand);
+    }
+    const float c0 = __shfl_up_sync(0xffffffffu, my_c, 1), l0 = __shfl_up_sync(0xffffffffu, l, 1);
+    const float b0 = __shfl_up_sync(0xffffffffu, bias, 1);
+    const bool near = lane > 0 && lane < m && !(l == l0 && bias == b0) &&
+                      !(c0 - my_c > (p.bias != nullptr ? slack : step * c0));
+    if (__any_sync(0xffffffffu, near)) {
+        // Again in fp64: one exponential per lane, and each candidate's rank.
+        // (A softmax's common divisor changes no order.)
+        sure = sure && (p.sigmoid || p.bias == nullptr);
+        const double s = p.sigmoid ? 1.0 / (1.0 + exp(-(double)l)) : exp((double)l - (double)top);
+        const double c = s + (double)bias;
+        int rank = lane < m ? 0 : 32;
+        for (int j = 0; j < m; ++j) {
+            const double o = __shfl_sync(0xffffffffu, c, j);
+            const int oe = __shfl_sync(0xffffffffu, cand, j);
+            if (lane < m && (o > c || (o == c && oe < cand))) ++rank;
+        }
+        int src = 31;
+        for (int j = 0; j < m; ++j)
+            if (__shfl_sync(0xffffffffu, rank, j) == lane) src = j;
+        const int e = __shfl_sync(0xffffffffu, cand, src);
+        l = __shfl_sync(0xffffffffu, l, src);
+        cand = lane < m ? e : -1;
+    }
+    const bool mine = lane < p.k && cand >= 0;
+    float s = 0.0f;
+    if (mine) s = p.sigmoid ? __fdividef(1.0f, 1.0f + expf(-l)) : expf(l - top) * inv;
+    sure = sure && !(mine && (s < 1e-30f || (!p.sigmoid && l < top - 30.0f)));
+    if (!__all_sync(0xffffffffu, sure)) {
+        route_exact<NI>(row, p, lane, my_e, my_w);
+        return;
+    }
+    float sum = s;
+    #pragma unroll
+    for (int off = 16; off >= 1; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+    my_e = mine ? cand : -1;
+    my_w = (p.renorm ? (sum > 0.0f ? s / sum : 0.0f) : s) * (float)p.scale;
+}
+
+template <typename T, int NI>
+__global__ void __launch_bounds__(256) route_topk_kernel(const T* __restrict__ logits, RouteParams p) {
+    grid_dependency_wait();
+    grid_dependents_launch();
+    const int lane = threadIdx.x & 31;
+    const int t = blockIdx.x * 8 + (threadIdx.x >> 5);
+    if (t >= p.T) return;
+    int e;
+    float w;
+    route_token<NI>(logits + (int64_t)t * p.ld, p, lane, e, w);
     if (lane < p.k) {
-        double w = my_s;
-        if (p.renorm) w = sum > 0.0 ? w / sum : 0.0;
-        p.idx[(int64_t)t * p.k + lane] = my_e;
-        p.weights[(int64_t)t * p.k + lane] = (float)(w * p.scale);
+        p.idx[(int64_t)t * p.k + lane] = e;
+        p.weights[(int64_t)t * p.k + lane] = w;
     }
 }
 
+// ---------------------------------------------------------------------------
 // The plan: slots (t, j) in the order of t * k + j, sorted stably by expert.
 //   offsets[e]    first row of expert e, offsets[E] the rows in use
 //   row_token[r]  token of row r (-1 from offsets[E] on)
 //   slot_row[s]   row of slot s (-1 for a slot without an expert)
-// One cluster: CTA c counts its share of the slots per warp and expert in
-// shared memory, the counts of the CTAs before it come over distributed
-// shared memory, and each slot's row is the expert's start + the earlier
-// CTAs' and warps' counts + its place in the warp.  No atomics order the
-// result: it is the same on every run.
-__global__ void __launch_bounds__(route::PLAN_THREADS)
-route_plan_kernel(const int32_t* __restrict__ idx, int slots, int k, int E, int32_t* __restrict__ offsets,
-                  int32_t* __restrict__ row_token, int32_t* __restrict__ slot_row) {
+// CTAS CTAs of a cluster (or one) count their shares of the slots per warp and
+// expert in shared memory, the counts of the CTAs before come over distributed
+// shared memory, and each slot's row is the expert's start + the earlier CTAs'
+// and warps' counts + its place in the warp.  Counts are added by atomics, but
+// no atomic orders the result: it is the same on every run.
+// ---------------------------------------------------------------------------
+template <int CTAS>
+__device__ __forceinline__ void plan_sync() {
+    if constexpr (CTAS > 1)
+        asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+    else
+        __syncthreads();
+}
+
+template <int CTAS>
+__device__ __forceinline__ void route_plan(const int32_t* idx, int slots, int k, int E, int32_t* __restrict__ offsets,
+                                           int32_t* __restrict__ row_token, int32_t* __restrict__ slot_row,
+                                           int32_t* smem) {
     using namespace route;
-    constexpr int WARPS = PLAN_THREADS / 32;
-    extern __shared__ int32_t plan_smem[];
-    int32_t* total = plan_smem;                       // [E] this CTA's counts
-    int32_t* start = total + MAX_E;                   // [E] first row of this CTA's slots of each expert
-    int32_t* cnt = start + MAX_E;                     // [WARPS][E] counts, then running starts
+    constexpr int STEPS = 4;                          // steps of 32 slots whose loads are in flight together
+    int32_t* total = smem;                            // [E] this CTA's counts
+    int32_t* start = total + MAX_E;                   // [E + 1] first row of each expert
+    int32_t* cnt = start + MAX_E + 32;                // [PLAN_WARPS][E] counts, then running starts
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    uint32_t rank;
-    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
-    // Shares of whole warp steps: CTA c has slots [s0, s1), warp w of it [a, b).
+    uint32_t rank = 0;
+    if constexpr (CTAS > 1) asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
     const int steps = (slots + 31) / 32;
-    const int per_cta = (steps + PLAN_CLUSTER - 1) / PLAN_CLUSTER;
-    const int per_warp = (per_cta + WARPS - 1) / WARPS;
-    const int c0 = (int)rank * per_cta, c1 = min(steps, c0 + per_cta);
+    const int per_cta = (steps + CTAS - 1) / CTAS, per_warp = (per_cta + PLAN_WARPS - 1) / PLAN_WARPS;
+    const int c0 = min(steps, (int)rank * per_cta), c1 = min(steps, c0 + per_cta);
     const int w0 = min(c1, c0 + warp * per_warp), w1 = min(c1, w0 + per_warp);
-    for (int i = threadIdx.x; i < WARPS * E; i += PLAN_THREADS) cnt[i] = 0;
+    for (int i = threadIdx.x; i < PLAN_WARPS * E; i += PLAN_THREADS) cnt[i] = 0;
     __syncthreads();
     int32_t* mine = cnt + warp * E;
-    for (int st = w0; st < w1; ++st) {
-        const int s = st * 32 + lane;
-        const int e = s < slots ? idx[s] : -1;
-        const bool on = e >= 0 && e < E;
-        const unsigned same = __match_any_sync(0xffffffffu, on ? e : -1);
-        if (on && lane == __ffs(same) - 1) mine[e] += __popc(same);
-        __syncwarp();
+    auto load = [&](int st, int (&e)[STEPS]) {
+        #pragma unroll
+        for (int i = 0; i < STEPS; ++i) {
+            const int s = (st + i) * 32 + lane;
+            e[i] = st + i < w1 && s < slots ? idx[s] : -1;
+            if (e[i] >= E) e[i] = -1;
+        }
+    };
+    for (int st = w0; st < w1; st += STEPS) {
+        int e[STEPS];
+        load(st, e);
+        #pragma unroll
+        for (int i = 0; i < STEPS; ++i)
+            if (e[i] >= 0) atomicAdd(mine + e[i], 1);
     }
     __syncthreads();
     for (int e = threadIdx.x; e < E; e += PLAN_THREADS) {
         int run = 0;
-        for (int w = 0; w < WARPS; ++w) {
+        #pragma unroll 8
+        for (int w = 0; w < PLAN_WARPS; ++w) {
             const int c = cnt[w * E + e];
             cnt[w * E + e] = run;
             run += c;
         }
         total[e] = run;
     }
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+    plan_sync<CTAS>();
     // Counts of the earlier CTAs and of all of them, per expert.
     for (int e = threadIdx.x; e < E; e += PLAN_THREADS) {
         int before = 0, all = 0;
-        for (int c = 0; c < PLAN_CLUSTER; ++c) {
-            uint32_t a;
-            int v;
-            asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(total + e)), "r"(c));
-            asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
-            if (c < (int)rank) before += v;
-            all += v;
+        if constexpr (CTAS > 1) {
+            #pragma unroll
+            for (int c = 0; c < CTAS; ++c) {
+                uint32_t a;
+                int v;
+                asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(total + e)), "r"(c));
+                asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+                before += c < (int)rank ? v : 0;
+                all += v;
+            }
+            // The scan below turns start[e] into the expert's first row; this
+            // CTA's own slots begin `before` later, kept in the warps' starts.
+            #pragma unroll 8
+            for (int w = 0; w < PLAN_WARPS; ++w) cnt[w * E + e] += before;
+        } else {
+            all = total[e];
         }
         start[e] = all;
-        for (int w = 0; w < WARPS; ++w) cnt[w * E + e] += before;
     }
     __syncthreads();
-    if (warp == 0) {                                  // exclusive scan of the experts' totals
+    if (warp == 0) {                                  // exclusive scan of the experts' counts
         int carry = 0;
         for (int e0 = 0; e0 < E; e0 += 32) {
             const int v = e0 + lane < E ? start[e0 + lane] : 0;
@@ -253,36 +508,77 @@ route_plan_kernel(const int32_t* __restrict__ idx, int slots, int k, int E, int3
                 const int y = __shfl_up_sync(0xffffffffu, x, off);
                 if (lane >= off) x += y;
             }
-            if (e0 + lane < E) start[e0 + lane] = carry + x - v;
+            if (e0 + lane < E) {
+                start[e0 + lane] = carry + x - v;
+                if (rank == 0) offsets[e0 + lane] = carry + x - v;
+            }
             carry += __shfl_sync(0xffffffffu, x, 31);
         }
-        if (rank == 0) {
-            __syncwarp();
-            for (int e = lane; e < E; e += 32) offsets[e] = start[e];
-            if (lane == 0) offsets[E] = carry;
+        if (lane == 0) {
+            start[E] = carry;
+            if (rank == 0) offsets[E] = carry;
         }
-        // rows without a slot
-        if (row_token != nullptr)
-            for (int r = carry + (int)rank * 32 + lane; r < slots; r += 32 * PLAN_CLUSTER) row_token[r] = -1;
     }
     __syncthreads();
-    for (int st = w0; st < w1; ++st) {
-        const int s = st * 32 + lane;
-        const int e = s < slots ? idx[s] : -1;
-        const bool on = e >= 0 && e < E;
-        const unsigned same = __match_any_sync(0xffffffffu, on ? e : -1);
-        int r = -1;
-        if (on) r = start[e] + mine[e] + __popc(same & ((1u << lane) - 1));
-        __syncwarp();
-        if (on && lane == __ffs(same) - 1) mine[e] += __popc(same);
-        __syncwarp();
-        if (s < slots) {
-            if (slot_row != nullptr) slot_row[s] = r;
-            if (on && row_token != nullptr) row_token[r] = s / k;
+    for (int64_t r = start[E] + (int64_t)rank * PLAN_THREADS + threadIdx.x; r < slots; r += PLAN_THREADS * CTAS)
+        row_token[r] = -1;                            // rows without a slot
+    for (int st = w0; st < w1; st += STEPS) {
+        int e[STEPS];
+        load(st, e);
+        #pragma unroll
+        for (int i = 0; i < STEPS; ++i) {
+            if (st + i >= w1) break;
+            const int s = (st + i) * 32 + lane;
+            const unsigned same = __match_any_sync(0xffffffffu, e[i]);
+            int r = -1;
+            if (e[i] >= 0) r = start[e[i]] + mine[e[i]] + __popc(same & ((1u << lane) - 1));
+            __syncwarp();
+            if (e[i] >= 0 && lane == __ffs(same) - 1) mine[e[i]] += __popc(same);
+            __syncwarp();
+            if (s < slots) {
+                slot_row[s] = r;
+                if (r >= 0) row_token[r] = s / k;
+            }
         }
     }
     // No CTA leaves while another may still read its counts.
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+    if constexpr (CTAS > 1) plan_sync<CTAS>();
+}
+
+constexpr int route_plan_smem(int E) { return (2 * route::MAX_E + 32 + route::PLAN_WARPS * E) * 4; }
+
+__global__ void __launch_bounds__(route::PLAN_THREADS)
+route_plan_kernel(const int32_t* idx, int slots, int k, int E, int32_t* __restrict__ offsets,
+                  int32_t* __restrict__ row_token, int32_t* __restrict__ slot_row) {
+    extern __shared__ int32_t plan_smem[];
+    grid_dependency_wait();
+    grid_dependents_launch();
+    route_plan<route::PLAN_CLUSTER>(idx, slots, k, E, offsets, row_token, slot_row, plan_smem);
+}
+
+// Choice and plan of up to SMALL_T tokens in one CTA: one launch for a decode step.
+template <typename T, int NI>
+__global__ void __launch_bounds__(route::PLAN_THREADS)
+route_small_kernel(const T* __restrict__ logits, RouteParams p, int32_t* __restrict__ offsets,
+                   int32_t* __restrict__ row_token, int32_t* __restrict__ slot_row) {
+    using namespace route;
+    extern __shared__ int32_t plan_smem[];
+    __shared__ int32_t chosen[SMALL_T * MAX_K];
+    grid_dependency_wait();
+    grid_dependents_launch();
+    const int lane = threadIdx.x & 31;
+    for (int t = threadIdx.x >> 5; t < p.T; t += PLAN_WARPS) {
+        int e;
+        float w;
+        route_token<NI>(logits + (int64_t)t * p.ld, p, lane, e, w);
+        if (lane < p.k) {
+            chosen[t * p.k + lane] = e;
+            p.idx[(int64_t)t * p.k + lane] = e;
+            p.weights[(int64_t)t * p.k + lane] = w;
+        }
+    }
+    __syncthreads();
+    route_plan<1>(chosen, p.T * p.k, p.k, p.E, offsets, row_token, slot_row, plan_smem);
 }
 
 // ---------------------------------------------------------------------------
