@@ -1969,6 +1969,8 @@ bool route_smem_configured() {
     using bf16 = __nv_bfloat16;
     if (cudaFuncSetAttribute(bnn::route_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              bnn::route_plan_smem(bnn::route::MAX_E)) != cudaSuccess ||
+        cudaFuncSetAttribute(bnn::route_plan_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) !=
+            cudaSuccess ||
         !route_small_opt_in<float, 2>() || !route_small_opt_in<float, 4>() || !route_small_opt_in<float, 8>() ||
         !route_small_opt_in<float, 16>() || !route_small_opt_in<bf16, 2>() || !route_small_opt_in<bf16, 4>() ||
         !route_small_opt_in<bf16, 8>() || !route_small_opt_in<bf16, 16>())

@@ -11,8 +11,8 @@ namespace route {
 constexpr int MAX_E = 512;
 constexpr int MAX_K = 16;
 constexpr int MAX_GROUPS = 32;
-constexpr int PLAN_CLUSTER = 8;
-constexpr int PLAN_THREADS = 1024;
+constexpr int PLAN_CLUSTER = 16;             // opt-in size: the scattered rows are bound by the SMs that write
+constexpr int PLAN_THREADS = 512;
 constexpr int PLAN_WARPS = PLAN_THREADS / 32;
 constexpr int SMALL_T = 16;                  // tokens that one CTA chooses for and plans in one launch
 }  // namespace route
@@ -41,14 +41,11 @@ __device__ __forceinline__ double key_value(unsigned long long q) {
     return __longlong_as_double((long long)((q >> 63) ? q & 0x7FFFFFFFFFFFFFFFull : ~q));
 }
 
-// Largest key of the warp and the lowest index that has it.
-__device__ __forceinline__ void warp_best(unsigned long long& key, int& id) {
-    #pragma unroll
-    for (int off = 16; off >= 1; off >>= 1) {
-        const unsigned long long k2 = __shfl_xor_sync(0xffffffffu, key, off);
-        const int i2 = __shfl_xor_sync(0xffffffffu, id, off);
-        if (k2 > key || (k2 == key && i2 < id)) { key = k2; id = i2; }
-    }
+// Largest key of the warp.
+__device__ __forceinline__ unsigned long long warp_max_key(unsigned long long key) {
+    const uint32_t hi = __reduce_max_sync(0xffffffffu, (uint32_t)(key >> 32));
+    const uint32_t lo = __reduce_max_sync(0xffffffffu, (uint32_t)(key >> 32) == hi ? (uint32_t)key : 0u);
+    return (unsigned long long)hi << 32 | lo;
 }
 __device__ __forceinline__ double warp_max(double v) {
     #pragma unroll
@@ -151,22 +148,19 @@ __device__ __noinline__ void route_exact(const T* __restrict__ row, const RouteP
                     else if (key[i] > k2) k2 = key[i];
                 }
             }
-            #pragma unroll
-            for (int off = 16; off >= 1; off >>= 1) {
-                const unsigned long long o1 = __shfl_xor_sync(0xffffffffu, k1, off);
-                const unsigned long long o2 = __shfl_xor_sync(0xffffffffu, k2, off);
-                if (o1 > k1) { k2 = max(k1, o2); k1 = o1; }
-                else k2 = max(k2, o1);
-            }
+            const unsigned long long t1 = warp_max_key(k1);
+            // The second: the winner's lane (one of them) offers its other.
+            const unsigned has = __ballot_sync(0xffffffffu, k1 == t1);
+            k2 = warp_max_key(lane == __ffs(has) - 1 ? k2 : k1);
+            k1 = t1;
             if (p.group_top > 1 && k2 != 0) k1 = order_key(key_value(k1) + key_value(k2));
             if (lane == g) mine = k1;
         }
         unsigned kept = 0;
         for (int j = 0; j < p.kept; ++j) {
-            unsigned long long b = mine;
-            int id = lane;
-            warp_best(b, id);
+            const unsigned long long b = warp_max_key(mine);
             if (b == 0) break;
+            const int id = __ffs(__ballot_sync(0xffffffffu, mine == b)) - 1;
             kept |= 1u << id;
             if (lane == id) mine = 0;
         }
@@ -181,15 +175,17 @@ __device__ __noinline__ void route_exact(const T* __restrict__ row, const RouteP
     double my_s = 0.0;
     for (int j = 0; j < p.k; ++j) {
         unsigned long long b = 0;
-        int id = 0x7fffffff;
+        int at = 0;
         double s = 0.0;
         #pragma unroll
         for (int i = 0; i < NI; ++i)
-            if (key[i] > b) { b = key[i]; id = lane * NI + i; s = score[i]; }
-        int win = id;
-        warp_best(b, win);
-        if (b == 0) break;
-        const double ws = __shfl_sync(0xffffffffu, s, win / NI);
+            if (key[i] > b) { b = key[i]; at = i; s = score[i]; }
+        const unsigned long long best = warp_max_key(b);
+        if (best == 0) break;
+        // The lowest lane's first is the lowest index.
+        const int from = __ffs(__ballot_sync(0xffffffffu, b == best)) - 1;
+        const int win = from * NI + __shfl_sync(0xffffffffu, at, from);
+        const double ws = __shfl_sync(0xffffffffu, s, from);
         if (lane == j) { my_e = win; my_s = ws; }
         #pragma unroll
         for (int i = 0; i < NI; ++i)
@@ -208,6 +204,37 @@ __device__ __forceinline__ uint32_t order_key(float v) {
 }
 __device__ __forceinline__ float key_value(uint32_t q) {
     return __uint_as_float((q >> 31) ? q & 0x7FFFFFFFu : ~q);
+}
+
+// Batcher's odd-even merge sort of N = 2^n values, as a list of compared pairs.
+template <int N>
+struct SortPairs {
+    int a[N * N], b[N * N], n;
+    constexpr SortPairs() : a{}, b{}, n(0) {
+        for (int p = 1; p < N; p *= 2)
+            for (int k = p; k >= 1; k /= 2)
+                for (int j = k % p; j + k < N; j += 2 * k)
+                    for (int i = 0; i < k && i + j + k < N; ++i)
+                        if ((i + j) / (2 * p) == (i + j + k) / (2 * p)) {
+                            a[n] = i + j;
+                            b[n++] = i + j + k;
+                        }
+    }
+};
+// Sorts a lane's keys, largest first, with their places (equal keys in any order).
+template <int NI>
+__device__ __forceinline__ void sort_keys(uint32_t (&key)[NI], uint32_t (&at)[NI]) {
+    constexpr SortPairs<NI> net;
+    #pragma unroll
+    for (int c = 0; c < net.n; ++c) {
+        const int a = net.a[c], b = net.b[c];
+        const bool swap = key[a] < key[b];
+        const uint32_t ka = key[a], pa = at[a];
+        key[a] = swap ? key[b] : ka;
+        at[a] = swap ? at[b] : pa;
+        key[b] = swap ? ka : key[b];
+        at[b] = swap ? pa : at[b];
+    }
 }
 
 // One warp, one token, lane l holding experts l * NI .. l * NI + NI - 1 (the
@@ -274,7 +301,8 @@ __device__ __forceinline__ void route_token(const T* __restrict__ row, const Rou
     if (p.kept < p.groups) {
         const int per = p.E / p.groups;
         uint32_t mine = 0;                                     // lane g: group g's score
-        if (per % NI == 0 && ((per / NI) & (per / NI - 1)) == 0) {
+        const bool whole = per % NI == 0 && ((per / NI) & (per / NI - 1)) == 0;
+        if (whole) {
             // Groups of whole lanes, a power of two of them.
             uint32_t k1 = 0, k2 = 0;
             #pragma unroll
@@ -319,36 +347,46 @@ __device__ __forceinline__ void route_token(const T* __restrict__ row, const Rou
         const uint32_t next = __reduce_max_sync(0xffffffffu, in ? 0u : mine);
         if (next != 0) sure = sure && key_value(least) - key_value(next) > 2.0f * slack;
         const unsigned kept = __ballot_sync(0xffffffffu, in);
-        #pragma unroll
-        for (int i = 0; i < NI; ++i) {
-            const int e = lane * NI + i;
-            if (e < p.E && ((kept >> (e / per)) & 1u) == 0) key[i] = 0;
+        if (whole) {                                           // (a lane's experts are one group's)
+            if (((kept >> (lane * NI / per)) & 1u) == 0) {
+                #pragma unroll
+                for (int i = 0; i < NI; ++i) key[i] = 0;
+            }
+        } else {
+            #pragma unroll
+            for (int i = 0; i < NI; ++i) {
+                const int e = lane * NI + i;
+                if (e < p.E && ((kept >> (e / per)) & 1u) == 0) key[i] = 0;
+            }
         }
     }
     // Candidates in order, the j-th to lane j: k of them, and on to the first
-    // that is certainly below.  Every lane offers its best, the winner's lane
-    // gives it up.  Without a bias the order is that of the scores, whose errors
+    // that is certainly below.  Every lane sorts its keys and offers the first,
+    // the winner's lane moves on.  Without a bias the order is that of the scores, whose errors
     // are relative: no score below has a larger one.
     const float step = 2.0f * rel;
     int cand = -1, m = 0;
     float my_c = 0.0f, last = 0.0f;
+    uint32_t at[NI];
+    #pragma unroll
+    for (int i = 0; i < NI; ++i) at[i] = lane * NI + i;
+    sort_keys<NI>(key, at);
     for (; m < 32; ++m) {
-        uint32_t b = 0;
-        int at = 0;
-        #pragma unroll
-        for (int i = 0; i < NI; ++i)
-            if (key[i] > b) { b = key[i]; at = i; }
-        const uint32_t best = __reduce_max_sync(0xffffffffu, b);
+        const uint32_t best = __reduce_max_sync(0xffffffffu, key[0]);
         if (best == 0) break;
         const float c = key_value(best);
         if (m >= p.k && last - c > (p.bias != nullptr ? slack : step * last)) break;
         last = c;
-        const int from = __ffs(__ballot_sync(0xffffffffu, b == best)) - 1;
-        const int win = from * NI + __shfl_sync(0xffffffffu, at, from);
+        const int from = __ffs(__ballot_sync(0xffffffffu, key[0] == best)) - 1;
+        const int win = __shfl_sync(0xffffffffu, at[0], from);
         if (lane == m) { cand = win; my_c = c; }
+        const bool mine = lane == from;
         #pragma unroll
-        for (int i = 0; i < NI; ++i)
-            if (lane * NI + i == win) key[i] = 0;
+        for (int i = 0; i + 1 < NI; ++i) {
+            key[i] = mine ? key[i + 1] : key[i];
+            at[i] = mine ? at[i + 1] : at[i];
+        }
+        if (mine) key[NI - 1] = 0;
     }
     sure = sure && (m < 32 || p.E <= 32);
     float l = 0.0f, bias = 0.0f;
@@ -358,7 +396,8 @@ __device__ __forceinline__ void route_token(const T* __restrict__ row, const Rou
     }
     const float c0 = __shfl_up_sync(0xffffffffu, my_c, 1), l0 = __shfl_up_sync(0xffffffffu, l, 1);
     const float b0 = __shfl_up_sync(0xffffffffu, bias, 1);
-    const bool near = lane > 0 && lane < m && !(l == l0 && bias == b0) &&
+    const int e0 = __shfl_up_sync(0xffffffffu, cand, 1);
+    const bool near = lane > 0 && lane < m && !(l == l0 && bias == b0 && e0 < cand) &&
                       !(c0 - my_c > (p.bias != nullptr ? slack : step * c0));
     if (__any_sync(0xffffffffu, near)) {
         // Again in fp64: one exponential per lane, and each candidate's rank.
@@ -394,8 +433,9 @@ __device__ __forceinline__ void route_token(const T* __restrict__ row, const Rou
     my_w = (p.renorm ? (sum > 0.0f ? s / sum : 0.0f) : s) * (float)p.scale;
 }
 
+// (Registers limited for occupancy: only route_exact() would take more.)
 template <typename T, int NI>
-__global__ void __launch_bounds__(256) route_topk_kernel(const T* __restrict__ logits, RouteParams p) {
+__global__ void __launch_bounds__(256, 4) route_topk_kernel(const T* __restrict__ logits, RouteParams p) {
     grid_dependency_wait();
     grid_dependents_launch();
     const int lane = threadIdx.x & 31;
@@ -434,10 +474,11 @@ __device__ __forceinline__ void route_plan(const int32_t* idx, int slots, int k,
                                            int32_t* __restrict__ row_token, int32_t* __restrict__ slot_row,
                                            int32_t* smem) {
     using namespace route;
-    constexpr int STEPS = 4;                          // steps of 32 slots whose loads are in flight together
+    constexpr int STEPS = 8;                          // steps of 32 slots whose loads are in flight together
     int32_t* total = smem;                            // [E] this CTA's counts
-    int32_t* start = total + MAX_E;                   // [E + 1] first row of each expert
-    int32_t* cnt = start + MAX_E + 32;                // [PLAN_WARPS][E] counts, then running starts
+    int32_t* start = total + MAX_E;                   // [E] first row of each expert's slots in this CTA
+    int32_t* part = start + MAX_E;                    // [32] sums of 32 experts
+    int32_t* cnt = part + 32;                         // [PLAN_WARPS][E], zero: counts, then starts within the CTA
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     uint32_t rank = 0;
     if constexpr (CTAS > 1) asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
@@ -445,28 +486,28 @@ __device__ __forceinline__ void route_plan(const int32_t* idx, int slots, int k,
     const int per_cta = (steps + CTAS - 1) / CTAS, per_warp = (per_cta + PLAN_WARPS - 1) / PLAN_WARPS;
     const int c0 = min(steps, (int)rank * per_cta), c1 = min(steps, c0 + per_cta);
     const int w0 = min(c1, c0 + warp * per_warp), w1 = min(c1, w0 + per_warp);
-    for (int i = threadIdx.x; i < PLAN_WARPS * E; i += PLAN_THREADS) cnt[i] = 0;
-    __syncthreads();
     int32_t* mine = cnt + warp * E;
-    auto load = [&](int st, int (&e)[STEPS]) {
+    int ex[STEPS];
+    auto load = [&](int st) {
         #pragma unroll
         for (int i = 0; i < STEPS; ++i) {
             const int s = (st + i) * 32 + lane;
-            e[i] = st + i < w1 && s < slots ? idx[s] : -1;
-            if (e[i] >= E) e[i] = -1;
+            ex[i] = st + i < w1 && s < slots ? idx[s] : -1;
+            if (ex[i] >= E) ex[i] = -1;
         }
     };
     for (int st = w0; st < w1; st += STEPS) {
-        int e[STEPS];
-        load(st, e);
+        load(st);
         #pragma unroll
         for (int i = 0; i < STEPS; ++i)
-            if (e[i] >= 0) atomicAdd(mine + e[i], 1);
+            if (ex[i] >= 0) atomicAdd(mine + ex[i], 1);
     }
     __syncthreads();
-    for (int e = threadIdx.x; e < E; e += PLAN_THREADS) {
-        int run = 0;
-        #pragma unroll 8
+    static_assert(PLAN_THREADS >= MAX_E, "a thread per expert");
+    const int e = threadIdx.x;
+    int run = 0;
+    if (e < E) {
+        #pragma unroll
         for (int w = 0; w < PLAN_WARPS; ++w) {
             const int c = cnt[w * E + e];
             cnt[w * E + e] = run;
@@ -475,65 +516,59 @@ __device__ __forceinline__ void route_plan(const int32_t* idx, int slots, int k,
         total[e] = run;
     }
     plan_sync<CTAS>();
-    // Counts of the earlier CTAs and of all of them, per expert.
-    for (int e = threadIdx.x; e < E; e += PLAN_THREADS) {
-        int before = 0, all = 0;
-        if constexpr (CTAS > 1) {
+    // Counts of the earlier CTAs and of all of them, and the scan over experts.
+    int before = 0, all = run;
+    if constexpr (CTAS > 1) {
+        if (e < E) {
+            int v[CTAS];
             #pragma unroll
             for (int c = 0; c < CTAS; ++c) {
                 uint32_t a;
-                int v;
                 asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(total + e)), "r"(c));
-                asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
-                before += c < (int)rank ? v : 0;
-                all += v;
+                asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v[c]) : "r"(a) : "memory");
             }
-            // The scan below turns start[e] into the expert's first row; this
-            // CTA's own slots begin `before` later, kept in the warps' starts.
-            #pragma unroll 8
-            for (int w = 0; w < PLAN_WARPS; ++w) cnt[w * E + e] += before;
-        } else {
-            all = total[e];
-        }
-        start[e] = all;
-    }
-    __syncthreads();
-    if (warp == 0) {                                  // exclusive scan of the experts' counts
-        int carry = 0;
-        for (int e0 = 0; e0 < E; e0 += 32) {
-            const int v = e0 + lane < E ? start[e0 + lane] : 0;
-            int x = v;
+            all = 0;
             #pragma unroll
-            for (int off = 1; off < 32; off <<= 1) {
-                const int y = __shfl_up_sync(0xffffffffu, x, off);
-                if (lane >= off) x += y;
+            for (int c = 0; c < CTAS; ++c) {
+                before += c < (int)rank ? v[c] : 0;
+                all += v[c];
             }
-            if (e0 + lane < E) {
-                start[e0 + lane] = carry + x - v;
-                if (rank == 0) offsets[e0 + lane] = carry + x - v;
-            }
-            carry += __shfl_sync(0xffffffffu, x, 31);
-        }
-        if (lane == 0) {
-            start[E] = carry;
-            if (rank == 0) offsets[E] = carry;
         }
     }
+    int incl = all;
+    #pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, incl, off);
+        if (lane >= off) incl += y;
+    }
+    if (lane == 31) part[warp] = incl;
     __syncthreads();
-    for (int64_t r = start[E] + (int64_t)rank * PLAN_THREADS + threadIdx.x; r < slots; r += PLAN_THREADS * CTAS)
+    int rows = 0;                                     // rows before this warp's experts, then in use
+    #pragma unroll
+    for (int w = 0; w < PLAN_WARPS; ++w) {
+        const int v = part[w];
+        if (w < warp) incl += v;
+        rows += v;
+    }
+    if (e < E) {
+        start[e] = incl - all + before;
+        if (rank == 0) offsets[e] = incl - all;
+    }
+    if (rank == 0 && threadIdx.x == 0) offsets[E] = rows;
+    __syncthreads();
+    for (int64_t r = rows + (int64_t)rank * PLAN_THREADS + threadIdx.x; r < slots; r += PLAN_THREADS * CTAS)
         row_token[r] = -1;                            // rows without a slot
     for (int st = w0; st < w1; st += STEPS) {
-        int e[STEPS];
-        load(st, e);
+        if (per_warp > STEPS) load(st);               // else the first pass's are still here
         #pragma unroll
         for (int i = 0; i < STEPS; ++i) {
             if (st + i >= w1) break;
             const int s = (st + i) * 32 + lane;
-            const unsigned same = __match_any_sync(0xffffffffu, e[i]);
+            const unsigned same = __match_any_sync(0xffffffffu, ex[i]);
             int r = -1;
-            if (e[i] >= 0) r = start[e[i]] + mine[e[i]] + __popc(same & ((1u << lane) - 1));
+            if (ex[i] >= 0) r = start[ex[i]] + mine[ex[i]] + __popc(same & ((1u << lane) - 1));
             __syncwarp();
-            if (e[i] >= 0 && lane == __ffs(same) - 1) mine[e[i]] += __popc(same);
+            if (ex[i] >= 0 && lane == __ffs(same) - 1) mine[ex[i]] += __popc(same);
             __syncwarp();
             if (s < slots) {
                 slot_row[s] = r;
@@ -545,12 +580,20 @@ __device__ __forceinline__ void route_plan(const int32_t* idx, int slots, int k,
     if constexpr (CTAS > 1) plan_sync<CTAS>();
 }
 
+// Zeroes the counts of route_plan (before its barrier; may run ahead of the inputs).
+__device__ __forceinline__ void route_plan_clear(int32_t* smem, int E) {
+    int32_t* cnt = smem + 2 * route::MAX_E + 32;
+    for (int i = threadIdx.x; i < route::PLAN_WARPS * E; i += route::PLAN_THREADS) cnt[i] = 0;
+    __syncthreads();
+}
+
 constexpr int route_plan_smem(int E) { return (2 * route::MAX_E + 32 + route::PLAN_WARPS * E) * 4; }
 
 __global__ void __launch_bounds__(route::PLAN_THREADS)
 route_plan_kernel(const int32_t* idx, int slots, int k, int E, int32_t* __restrict__ offsets,
                   int32_t* __restrict__ row_token, int32_t* __restrict__ slot_row) {
     extern __shared__ int32_t plan_smem[];
+    route_plan_clear(plan_smem, E);
     grid_dependency_wait();
     grid_dependents_launch();
     route_plan<route::PLAN_CLUSTER>(idx, slots, k, E, offsets, row_token, slot_row, plan_smem);
@@ -564,6 +607,7 @@ route_small_kernel(const T* __restrict__ logits, RouteParams p, int32_t* __restr
     using namespace route;
     extern __shared__ int32_t plan_smem[];
     __shared__ int32_t chosen[SMALL_T * MAX_K];
+    route_plan_clear(plan_smem, p.E);
     grid_dependency_wait();
     grid_dependents_launch();
     const int lane = threadIdx.x & 31;
