@@ -5,8 +5,8 @@
 // (4 exponent bits, 3 mantissa bits, largest value 448, NaN 0x7F, no
 // infinities): s = max(amax / 448, 2^-126) with amax the largest finite |x| of
 // the block, so the largest element lands on 448 and no quotient is larger.
-// The quotient is taken as x * (1 / s), both roundings in fp32 (each 2^-24,
-// against the 2^-4 of the code itself).  Blocks are 1 x 128 (activations: one
+// The quotient is that of x * 448 by amax, both rounded to fp32 (2^-24 each,
+// the product of a bf16 x none, against the 2^-4 of the code itself).  Blocks are 1 x 128 (activations: one
 // row's 128 consecutive elements of K) or 128 x 128 (weights).  The scale of
 // row block i and K block b is scales[b * ld + i]: a product walks K block by
 // block and then reads consecutive rows' scales together.
@@ -25,9 +25,47 @@ constexpr float SCALE_MIN = 1.17549435e-38f;   // 2^-126: the reciprocal stays f
 __device__ __forceinline__ float block_scale(float amax) { return fmaxf(__fdiv_rn(amax, CODE_MAX), SCALE_MIN); }
 
 // Two codes of a, b (a in the low byte); NaN gives the NaN code.
-__device__ __forceinline__ uint32_t codes2(float a, float b) {
-    return (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+__device__ __forceinline__ uint32_t codes2(float2 v) {
+    return (uint32_t)__nv_cvt_float2_to_fp8x2(v, __NV_SATFINITE, __NV_E4M3);
 }
+
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    float2 d;
+    asm("mul.rn.f32x2 %0, %1, %2;"
+        : "=l"(reinterpret_cast<unsigned long long&>(d))
+        : "l"(reinterpret_cast<unsigned long long&>(a)), "l"(reinterpret_cast<unsigned long long&>(b)));
+    return d;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;"
+        : "=l"(reinterpret_cast<unsigned long long&>(d))
+        : "l"(reinterpret_cast<unsigned long long&>(a)), "l"(reinterpret_cast<unsigned long long&>(b)),
+          "l"(reinterpret_cast<unsigned long long&>(c)));
+    return d;
+}
+
+// x * 448 / amax as x * m / d: d is amax's significand in [1, 2) and m = 448 *
+// 2^-exponent, so that nothing over- or underflows that matters; 2^126 and 1
+// where the scale is 2^-126.
+struct Quotient {
+    float m, d, inv;                        // inv = 1 / d, rounded
+    __device__ __forceinline__ void set(float amax) {
+        const uint32_t b = __float_as_uint(amax), e = b >> 23;
+        const bool least = amax < 448.0f * SCALE_MIN;
+        m = least ? 0x1p126f : __uint_as_float((262u - e) << 23 | 0x600000u);
+        d = least ? 1.0f : __uint_as_float((b & 0x7FFFFFu) | 0x3F800000u);
+    }
+    // Two quotients of y = x m, each rounded once: q = y inv is off by two units
+    // at most, its remainder q d - y is exact in one fused multiply-add, and q -
+    // remainder * inv rounds correctly (Markstein, IBM J. Res. Dev. 34, 1990);
+    // written so that a zero keeps its sign.
+    __device__ __forceinline__ float2 of(float2 x) const {
+        const float2 i2 = make_float2(-inv, -inv);
+        const float2 ny = mul2(x, make_float2(-m, -m)), q = mul2(ny, i2);
+        return fma2(fma2(q, make_float2(d, d), ny), i2, q);
+    }
+};
 
 // 32 bytes, read-only and not kept in L1 (one access where a row's lanes would
 // otherwise touch every 32-byte sector twice).
@@ -99,20 +137,22 @@ struct Elems {
         }
         return a;
     }
-    // 16 codes of x * inv.  SPECIAL (the block holds an infinity): x * 0 is 0
-    // for a finite x and NaN for an infinity, which then gets the NaN code.
+    // 16 codes.  SPECIAL (the block holds an infinity or nothing but NaN): x * 0
+    // is 0 for a finite x and NaN otherwise, which then gets the NaN code.
     template <bool SPECIAL>
-    __device__ __forceinline__ uint4 codes(float inv) const {
+    __device__ __forceinline__ uint4 codes(const Quotient& by) const {
         uint32_t o[4];
         #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            float q[4];
+            uint32_t c[2];
             #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float v = value(4 * i + j);
-                q[j] = SPECIAL ? fmaf(v, 0.0f, v * inv) : v * inv;
+            for (int j = 0; j < 2; ++j) {
+                const float2 v = make_float2(value(4 * i + 2 * j), value(4 * i + 2 * j + 1));
+                float2 q = by.of(v);
+                if constexpr (SPECIAL) q = make_float2(fmaf(v.x, 0.0f, q.x), fmaf(v.y, 0.0f, q.y));
+                c[j] = codes2(q);
             }
-            o[i] = codes2(q[0], q[1]) | (codes2(q[2], q[3]) << 16);
+            o[i] = c[0] | (c[1] << 16);
         }
         return make_uint4(o[0], o[1], o[2], o[3]);
     }
@@ -181,17 +221,22 @@ struct Narrow {
         return a;
     }
     // Codes to columns below `np` (n rounded up to 16) of the block's row.
-    __device__ __forceinline__ void store(uint8_t* p, int np, int lane, float inv, bool special) const {
-        float q[4];
+    __device__ __forceinline__ void store(uint8_t* p, int np, int lane, const Quotient& by, bool special) const {
+        float2 q[2];
         #pragma unroll
-        for (int i = 0; i < 4; ++i) q[i] = special ? fmaf(v[i], 0.0f, v[i] * inv) : v[i] * inv;
+        for (int i = 0; i < 2; ++i) {
+            q[i] = by.of(make_float2(v[2 * i], v[2 * i + 1]));
+            if (special) q[i] = make_float2(fmaf(v[2 * i], 0.0f, q[i].x), fmaf(v[2 * i + 1], 0.0f, q[i].y));
+        }
+        const uint32_t lo = codes2(q[0]), hi = codes2(q[1]);
         #pragma unroll
         for (int i = 0; i < 4; i += V) {
             const int c = column(i, lane);
             if (c >= np) continue;
-            if constexpr (V == 1) p[c] = (uint8_t)codes2(q[i], 0.0f);
-            else if constexpr (V == 2) *reinterpret_cast<uint16_t*>(p + c) = (uint16_t)codes2(q[i], q[i + 1]);
-            else *reinterpret_cast<uint32_t*>(p + c) = codes2(q[0], q[1]) | (codes2(q[2], q[3]) << 16);
+            const uint32_t two = i < 2 ? lo : hi;
+            if constexpr (V == 1) p[c] = (uint8_t)((i & 1) ? two >> 8 : two);
+            else if constexpr (V == 2) *reinterpret_cast<uint16_t*>(p + c) = (uint16_t)two;
+            else *reinterpret_cast<uint32_t*>(p + c) = lo | (hi << 16);
         }
     }
 };
@@ -254,14 +299,19 @@ fp8_pack_rows_kernel(const T* __restrict__ x, int64_t x_rows, int64_t K, int64_t
                 if ((lane & (LANES - 1)) == u) a = m;
             }
         }
-        const float s = block_scale(a), inv = __frcp_rn(s);
+        const float s = block_scale(a);
+        Quotient by;
+        by.set(a);
+        const float inv = __frcp_rn(by.d);
         #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int64_t c = c0 + u * 512;
-            const float f = __shfl_sync(0xffffffffu, inv, (lane & ~(LANES - 1)) | u);
+            const int from = (lane & ~(LANES - 1)) | u;
+            by.set(__shfl_sync(0xffffffffu, a, from));
+            by.inv = __shfl_sync(0xffffffffu, inv, from);
             if (c < K)
                 *reinterpret_cast<uint4*>(codes + r * ldc + c) =
-                    special ? v[u].template codes<true>(f) : v[u].template codes<false>(f);
+                    special ? v[u].template codes<true>(by) : v[u].template codes<false>(by);
         }
         // Lane u of the eight writes the scale of the block in its u-th vector.
         const int64_t cs = c0 - lane * 16 + (lane & ~(LANES - 1)) * 16 + (lane & (LANES - 1)) * 512;
@@ -316,12 +366,16 @@ fp8_pack_rows_narrow_kernel(const T* __restrict__ x, int64_t x_rows, int64_t K, 
                 if (lane == u) a = m;
             }
         }
-        const float s = block_scale(a), inv = __frcp_rn(s);
+        const float s = block_scale(a);
+        Quotient by;
+        by.set(a);
+        const float inv = __frcp_rn(by.d);
         #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const float f = __shfl_sync(0xffffffffu, inv, u);
+            by.set(__shfl_sync(0xffffffffu, a, u));
+            by.inv = __shfl_sync(0xffffffffu, inv, u);
             const int64_t n = (K + 15) / 16 * 16 - (b0 + u) * BLOCK;
-            v[u].store(codes + r * ldc + (b0 + u) * BLOCK, n < BLOCK ? (n < 0 ? 0 : (int)n) : BLOCK, lane, f, special);
+            v[u].store(codes + r * ldc + (b0 + u) * BLOCK, n < BLOCK ? (n < 0 ? 0 : (int)n) : BLOCK, lane, by, special);
         }
         if (lane < U && (b0 + lane) * BLOCK < K) scales[(b0 + lane) * lds + r] = s;
     }
@@ -361,13 +415,16 @@ fp8_pack_blocks_kernel(const T* __restrict__ x, int64_t rows, int64_t K, int64_t
     __syncthreads();
     #pragma unroll
     for (int w = 0; w < 8; ++w) a = fmaxf(a, part[w]);
-    const float s = block_scale(a), inv = __frcp_rn(s);
+    const float s = block_scale(a);
+    Quotient by;
+    by.set(a);
+    by.inv = __frcp_rn(by.d);
     #pragma unroll
     for (int u = 0; u < U; ++u) {
         const int64_t r = r0 + 32 * u;
         if (r < rows && c < K)
             *reinterpret_cast<uint4*>(codes + r * ldc + c) =
-                special ? v[u].template codes<true>(inv) : v[u].template codes<false>(inv);
+                special ? v[u].template codes<true>(by) : v[u].template codes<false>(by);
     }
     if (threadIdx.x == 0) scales[kb * lds + rb] = s;
 }
@@ -408,11 +465,14 @@ fp8_pack_blocks_narrow_kernel(const T* __restrict__ x, int64_t rows, int64_t K, 
     __syncthreads();
     #pragma unroll
     for (int w = 0; w < 8; ++w) a = fmaxf(a, part[w]);
-    const float s = block_scale(a), inv = __frcp_rn(s);
+    const float s = block_scale(a);
+    Quotient by;
+    by.set(a);
+    by.inv = __frcp_rn(by.d);
     #pragma unroll
     for (int u = 0; u < U; ++u) {
         const int64_t r = r0 + 8 * u;
-        if (r < rows) v[u].store(codes + r * ldc + kb * BLOCK, (n + 15) / 16 * 16, lane, inv, special);
+        if (r < rows) v[u].store(codes + r * ldc + kb * BLOCK, (n + 15) / 16 * 16, lane, by, special);
     }
     if (threadIdx.x == 0) scales[kb * lds + rb] = s;
 }

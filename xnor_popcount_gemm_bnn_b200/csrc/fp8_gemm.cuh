@@ -124,7 +124,7 @@ __device__ __forceinline__ void mbar_arrive_relaxed(uint32_t addr) {
 }
 
 // acc += t * s on pairs of fp32 (one instruction per two products).
-__device__ __forceinline__ void fma2(float2& acc, float2 t, float2 s) {
+__device__ __forceinline__ void scale_add2(float2& acc, float2 t, float2 s) {
     asm("fma.rn.f32x2 %0, %1, %2, %0;"
         : "+l"(reinterpret_cast<unsigned long long&>(acc))
         : "l"(reinterpret_cast<unsigned long long&>(t)), "l"(reinterpret_cast<unsigned long long&>(s)));
@@ -357,9 +357,9 @@ fp8_gemm_split_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_cons
                     #pragma unroll
                     for (int j = 0; j < CH; j += 4) {
                         const float4 f = *reinterpret_cast<const float4*>(s + c + j);
-                        fma2(acc[(c + j) / 2], make_float2(__uint_as_float(r[j]), __uint_as_float(r[j + 1])),
+                        scale_add2(acc[(c + j) / 2], make_float2(__uint_as_float(r[j]), __uint_as_float(r[j + 1])),
                              make_float2(f.x, f.y));
-                        fma2(acc[(c + j) / 2 + 1], make_float2(__uint_as_float(r[j + 2]), __uint_as_float(r[j + 3])),
+                        scale_add2(acc[(c + j) / 2 + 1], make_float2(__uint_as_float(r[j + 2]), __uint_as_float(r[j + 3])),
                              make_float2(f.z, f.w));
                     }
                 }
@@ -739,7 +739,7 @@ fp8_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
                     tmem_ld16_sync(tq + b * BN + c, r);
                     #pragma unroll
                     for (int j = 0; j < 16; j += 2)
-                        fma2(acc[(c + j) / 2], make_float2(__uint_as_float(r[j]), __uint_as_float(r[j + 1])), s);
+                        scale_add2(acc[(c + j) / 2], make_float2(__uint_as_float(r[j]), __uint_as_float(r[j + 1])), s);
                 }
                 tc_fence_before();
                 // The loads have completed (wait::ld) and the scale was used: nothing
