@@ -115,6 +115,21 @@ __device__ __forceinline__ bool f8_wait_all(uint64_t* bar, uint32_t parity, vola
     return __all_sync(0xffffffffu, tc_wait(bar, parity, abort_flag));
 }
 
+// Whether the phase of parity `parity` is complete, without waiting.  Asked for
+// the next K block while this one's work goes on, it hides what a wait costs
+// even when there is nothing to wait for (about 180 cycles with the vote).
+__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+
 // Arrive on an mbarrier given by its address in the cluster's shared memory,
 // without ordering earlier memory operations (a release over the cluster costs
 // about a thousand cycles here): for an arrival that only says that values
@@ -446,9 +461,9 @@ fp8_gemm_split_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_cons
 namespace f8p {
 constexpr int BM = 128;                      // rows of A per CTA = TMEM lanes
 constexpr int A_BYTES = BM * fp8::BLOCK;     // 16 KiB per stage
-constexpr int WARP_PRODUCER = 0, WARP_MMA = 1, WARP_SCALE = 2, WARP_EPI0 = 4, EPI_WARPS = 16;
+constexpr int WARP_PRODUCER = 0, WARP_MMA = 1, WARP_SCALE = 2, SCALE_WARPS = 2, WARP_EPI0 = 4, EPI_WARPS = 8;
 constexpr int THREADS = (WARP_EPI0 + EPI_WARPS) * 32;
-constexpr int AHEAD = 4;                     // K blocks whose scales are in flight
+constexpr int AHEAD = 4;                     // K blocks whose scales a scale warp has in flight
 constexpr int OUT_ROW = 64;                  // bytes per row of an epilogue warp's staging block
 constexpr int OUT_BLOCK = 32 * OUT_ROW;
 constexpr int BAND = 8;                      // row tiles that a band of concurrent tiles spans
@@ -458,7 +473,7 @@ struct Cfg {
     static constexpr int STAGE = A_BYTES + W_BYTES;
     static constexpr int NBUF = 512 / BN;                    // accumulators in tensor memory
     static constexpr int NBK = BN / fp8::BLOCK;              // column blocks of a tile
-    static constexpr int RAW_BYTES = AHEAD * (4 + NBK) * 32 * 4;
+    static constexpr int RAW_BYTES = SCALE_WARPS * AHEAD * (4 + NBK) * 32 * 4;
     static constexpr int PROD_BYTES = 2 * NBUF * NBK * BM * 4;
     static constexpr int FIXED = EPI_WARPS * OUT_BLOCK + RAW_BYTES + PROD_BYTES + 512 + 1024;
     static constexpr int STAGES = (tc::SMEM_LIMIT - FIXED) / STAGE;
@@ -546,18 +561,17 @@ struct Fp8Tiles {
 //             weight rows per K block, counted on the even CTA's barrier.
 //  warp 1     in the even CTA issues the four MMAs of a K block (M = 256,
 //             N = BN) for both.
-//  warp 2     scales: per K block sA[b, row] * sW[b, column block] for the
-//             CTA's rows and the tile's column blocks, copied AHEAD blocks
-//             ahead and put into shared memory; its arrival on the
+//  warps 2-3  scales, taking turns: per K block sA[b, row] * sW[b, column
+//             block] for the CTA's rows and the tile's column blocks, copied
+//             ahead and put into shared memory; the arrival on the
 //             accumulator's barrier goes with the MMAs' commit.
-//  warps 4-19 epilogue: four warps per quadrant of 32 rows, a quarter of the
-//             columns each; thread = one row, BN / 4 fp32 sums in registers,
+//  warps 4-11 epilogue: two warps per quadrant of 32 rows, half of the columns
+//             each; thread = one row, BN / 2 fp32 sums in registers,
 //             C += scale * inner, one scale per thread and block.
 // The tensor memory holds 512 / BN accumulators: the MMAs of the next blocks
 // run while the epilogue adds this one.  What bounds the kernel is the
-// epilogue's latency per block (wait, tensor-memory load, multiply-add, hand
-// back), which is why its loop holds nothing else and four warps per scheduler
-// take turns.  The finished tile is rounded, put into shared memory (16-byte
+// latency of each role's loop per block (wait, issue, hand on), which is why
+// the loops hold nothing else and ask for the next block's barriers early.  The finished tile is rounded, put into shared memory (16-byte
 // chunks swizzled by row, no bank conflicts) and stored by row, rows and
 // columns outside left out.
 template <int BN, typename T>
@@ -571,7 +585,7 @@ fp8_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
     extern __shared__ uint8_t smem_raw[];
     uint8_t* ring = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     uint8_t* oring = ring + STAGES * C::STAGE;
-    float* raw = reinterpret_cast<float*>(oring + EPI_WARPS * OUT_BLOCK);  // [AHEAD][4 + NBK][32]
+    float* raw = reinterpret_cast<float*>(oring + EPI_WARPS * OUT_BLOCK);  // [SCALE_WARPS][AHEAD][4 + NBK][32]
     float* prod = raw + C::RAW_BYTES / 4;                                  // [2 NBUF][NBK][BM]
     uint64_t* full = reinterpret_cast<uint64_t*>(prod + C::PROD_BYTES / 4);
     uint64_t* empty = full + STAGES;
@@ -643,14 +657,18 @@ fp8_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
             // Stages lie 16-byte units apart in the descriptor's address field
             // (a shared-memory address never carries out of it).
             const uint64_t adesc = umma_desc_sw128(smem_u32(ring));
+            bool ready = false;                        // the next block's stage and accumulator
             for (int t = cid; ok && tiles.find(g, lane, t, tl); t += ncl) {
                 for (int kb = 0; kb < nk; ++kb, ++it) {
                     const uint32_t s = it % STAGES, b = it % NBUF;
                     const uint64_t da = adesc + (uint64_t)(s * (C::STAGE >> 4)), dw = da + (A_BYTES >> 4);
-                    ok = f8_wait_all(&full[s], (it / STAGES) & 1, abort_flag) &&
-                         (it < NBUF || f8_wait_all(&tempty[b], ((it / NBUF) - 1) & 1, abort_flag));
+                    ok = ready || (f8_wait_all(&full[s], (it / STAGES) & 1, abort_flag) &&
+                                   (it < NBUF || f8_wait_all(&tempty[b], ((it / NBUF) - 1) & 1, abort_flag)));
                     if (!ok) break;
                     tc_fence_after();
+                    const uint32_t nx = it + 1;
+                    const bool f = mbar_test(&full[nx % STAGES], (nx / STAGES) & 1);
+                    const bool e = nx < NBUF || mbar_test(&tempty[nx % NBUF], ((nx / NBUF) - 1) & 1);
                     if (elect_one()) {
                         #pragma unroll
                         for (int kk = 0; kk < 4; ++kk)
@@ -659,7 +677,7 @@ fp8_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
                         f4_commit<true>(&tfull[b], 0x3);
                         f4_commit<true>(&empty[s], 0x3);
                     }
-                    __syncwarp();
+                    ready = __all_sync(0xffffffffu, f && e);
                 }
             }
             if (elect_one()) {
@@ -668,7 +686,9 @@ fp8_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
             }
             __syncwarp();
         }
-    } else if (warp == WARP_SCALE) {
+    } else if (warp < WARP_EPI0) {
+        const int sw_id = warp - WARP_SCALE;           // takes the blocks whose `it` is this modulo SCALE_WARPS
+        float* mine = raw + sw_id * AHEAD * (4 + NBK) * 32 + lane;
         for (int t = cid; ok && tiles.find(g, lane, t, tl); t += ncl) {
             // Rows and columns past the ends take the last one's scale; they are not stored.
             const float* sa[4];
@@ -681,7 +701,7 @@ fp8_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
             // Every lane copies what it needs itself, so only its own copies are waited for.
             auto load = [&](int kb) {
                 if (kb < nk) {
-                    float* d = raw + (kb % AHEAD) * (4 + NBK) * 32 + lane;
+                    float* d = mine + (kb / SCALE_WARPS % AHEAD) * (4 + NBK) * 32;
                     #pragma unroll
                     for (int i = 0; i < 4; ++i) cp_async4(d + 32 * i, sa[i] + kb * g.ldsa);
                     #pragma unroll
@@ -689,18 +709,21 @@ fp8_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
                 }
                 cp_async_commit();
             };
+            const uint32_t it0 = it;
+            const int first = (int)((uint32_t)(sw_id - (int)it0) % SCALE_WARPS);
             #pragma unroll
-            for (int i = 0; i < AHEAD - 1; ++i) load(i);
-            for (int kb = 0; kb < nk; ++kb, ++it) {
+            for (int i = 0; i < AHEAD - 1; ++i) load(first + i * SCALE_WARPS);
+            for (int kb = first; kb < nk; kb += SCALE_WARPS) {
+                it = it0 + kb;
                 const uint32_t b = it % NBUF;
-                load(kb + AHEAD - 1);
+                load(kb + (AHEAD - 1) * SCALE_WARPS);
                 cp_async_wait<AHEAD - 1>();
                 // The accumulator's previous use is committed: its barrier can
                 // take this block's arrival, and the epilogue is done with the
                 // block 2 NBUF before this one (the MMAs had waited for it).
                 ok = it < NBUF || f8_wait_all(&tfull[b], ((it / NBUF) - 1) & 1, abort_flag);
                 if (!ok) break;
-                const float* d = raw + (kb % AHEAD) * (4 + NBK) * 32 + lane;
+                const float* d = mine + (kb / SCALE_WARPS % AHEAD) * (4 + NBK) * 32;
                 float* p = prod + (it % (2 * NBUF)) * NBK * BM + lane;
                 #pragma unroll
                 for (int n = 0; n < NBK; ++n) {
@@ -711,6 +734,7 @@ fp8_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&tfull[b]);
             }
+            it = it0 + nk;
         }
     } else if (warp >= WARP_EPI0) {
         const int quad = warp & 3, part = (warp - WARP_EPI0) >> 2;
@@ -719,6 +743,7 @@ fp8_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
         const float* sp = prod + part * CW / fp8::BLOCK * BM + 32 * quad + lane;
         const uint32_t tq = tmem_base + ((uint32_t)(32 * quad) << 16) + part * CW;
         T* out = static_cast<T*>(g.out);
+        bool ready = false;                            // the next accumulator and its scales
         for (int t = cid; ok && tiles.find(g, lane, t, tl); t += ncl) {
             const int mq = tl.m0 + (int)rank * BM + 32 * quad;       // first row of this warp
             const int nh = tl.n0 + part * CW;                        // first column
@@ -728,15 +753,17 @@ fp8_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
             #pragma unroll 1
             for (int kb = 0; kb < nk; ++kb, ++it) {
                 const uint32_t b = it % NBUF;
-                ok = f8_wait_all(&tfull[b], (it / NBUF) & 1, abort_flag);
+                ok = ready || f8_wait_all(&tfull[b], (it / NBUF) & 1, abort_flag);
                 if (!ok) break;
                 tc_fence_after();
                 const float f = sp[(it % (2 * NBUF)) * NBK * BM];
                 const float2 s = make_float2(f, f);
+                bool next = false;
                 #pragma unroll
                 for (int c = 0; c < CW; c += 16) {
                     uint32_t r[16];
                     tmem_ld16_sync(tq + b * BN + c, r);
+                    if (c + 32 == CW) next = mbar_test(&tfull[(it + 1) % NBUF], ((it + 1) / NBUF) & 1);
                     #pragma unroll
                     for (int j = 0; j < 16; j += 2)
                         scale_add2(acc[(c + j) / 2], make_float2(__uint_as_float(r[j]), __uint_as_float(r[j + 1])), s);
@@ -745,6 +772,7 @@ fp8_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
                 // The loads have completed (wait::ld) and the scale was used: nothing
                 // of this block is read after the arrival.
                 if (elect_one()) mbar_arrive_relaxed(hand_back + b * 8);
+                ready = __all_sync(0xffffffffu, next);
             }
             if (!ok) break;
             // 32 rows x 64 bytes at a time: chunk q of row r at (q ^ (r >> 1 & 3)) * 16.
