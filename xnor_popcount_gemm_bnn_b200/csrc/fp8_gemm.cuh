@@ -96,6 +96,32 @@ __device__ __forceinline__ bool elect_one() {
         : "=r"(p));
     return p != 0;
 }
+// TMEM -> registers in two statements, so that arithmetic runs between them: the
+// load is started, and the wait names the registers, which hold their values
+// only after it (every use has to come through the wait's outputs).
+__device__ __forceinline__ void tmem_ld32_start(uint32_t taddr, uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+          "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_ld32_wait(uint32_t (&r)[32]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]),
+                   "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]),
+                   "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]),
+                   "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
+                 :
+                 : "memory");
+}
+
 __device__ __forceinline__ void cp_async4(void* dst, const void* src) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
 }
@@ -628,115 +654,121 @@ fp8_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
     Fp8Tile tl;
     uint32_t it = 0;
     bool ok = true;
-    if (warp == WARP_PRODUCER) {
-        uint32_t issued = 0;
-        for (int t = cid; ok && tiles.find(g, lane, t, tl); t += ncl) {
-            for (int kb = 0; kb < nk; ++kb, ++it) {
-                const uint32_t s = it % STAGES;
-                ok = it < STAGES || f8_wait_all(&empty[s], ((it / STAGES) - 1) & 1, abort_flag);
-                if (!ok) break;
-                if (elect_one()) {
-                    uint8_t* dst = ring + s * C::STAGE;
-                    const uint32_t bar = mapa_shared(smem_u32(&full[s]), 0);
-                    if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * C::STAGE);
-                    tma_load_2d_pair(dst, &tmA, kb * fp8::BLOCK, tl.m0 + (int)rank * BM, bar);
-                    tma_load_3d_pair(dst + A_BYTES, &tmW, kb * fp8::BLOCK, tl.n0 + (int)rank * (BN / 2), tl.e, bar);
-                }
-                __syncwarp();
-                ++issued;
-            }
-        }
-        // After a failed wait: both CTAs' copies count on the even CTA's barriers.
-        if (lane == 0 && !ok && rank == 0) {
-            for (uint32_t q = issued > STAGES ? issued - STAGES : 0; q < issued; ++q)
-                if (!mbar_wait_bounded(&full[q % STAGES], (q / STAGES) & 1)) break;
-        }
-        __syncwarp();
-    } else if (warp == WARP_MMA) {
-        if (rank == 0) {
-            // Stages lie 16-byte units apart in the descriptor's address field
-            // (a shared-memory address never carries out of it).
-            const uint64_t adesc = umma_desc_sw128(smem_u32(ring));
-            bool ready = false;                        // the next block's stage and accumulator
+    // The epilogue's sums and the loads beside them take more registers than the
+    // other four warps: 128 * 80 + 256 * 208 of the launch's 384 * 168.
+    if (warp < WARP_EPI0) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+        if (warp == WARP_PRODUCER) {
+            uint32_t issued = 0;
             for (int t = cid; ok && tiles.find(g, lane, t, tl); t += ncl) {
                 for (int kb = 0; kb < nk; ++kb, ++it) {
-                    const uint32_t s = it % STAGES, b = it % NBUF;
-                    const uint64_t da = adesc + (uint64_t)(s * (C::STAGE >> 4)), dw = da + (A_BYTES >> 4);
-                    ok = ready || (f8_wait_all(&full[s], (it / STAGES) & 1, abort_flag) &&
-                                   (it < NBUF || f8_wait_all(&tempty[b], ((it / NBUF) - 1) & 1, abort_flag)));
+                    const uint32_t s = it % STAGES;
+                    ok = it < STAGES || f8_wait_all(&empty[s], ((it / STAGES) - 1) & 1, abort_flag);
                     if (!ok) break;
-                    tc_fence_after();
-                    const uint32_t nx = it + 1;
-                    const bool f = mbar_test(&full[nx % STAGES], (nx / STAGES) & 1);
-                    const bool e = nx < NBUF || mbar_test(&tempty[nx % NBUF], ((nx / NBUF) - 1) & 1);
                     if (elect_one()) {
-                        #pragma unroll
-                        for (int kk = 0; kk < 4; ++kk)
-                            mma_f8<2>(tmem_base + b * BN, da + kk * 2, dw + kk * 2, f8_idesc(2 * BM, BN),
-                                      kk != 0 ? 1u : 0u);
-                        f4_commit<true>(&tfull[b], 0x3);
-                        f4_commit<true>(&empty[s], 0x3);
+                        uint8_t* dst = ring + s * C::STAGE;
+                        const uint32_t bar = mapa_shared(smem_u32(&full[s]), 0);
+                        if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * C::STAGE);
+                        tma_load_2d_pair(dst, &tmA, kb * fp8::BLOCK, tl.m0 + (int)rank * BM, bar);
+                        tma_load_3d_pair(dst + A_BYTES, &tmW, kb * fp8::BLOCK, tl.n0 + (int)rank * (BN / 2), tl.e, bar);
                     }
-                    ready = __all_sync(0xffffffffu, f && e);
+                    __syncwarp();
+                    ++issued;
                 }
             }
-            if (elect_one()) {
-                f4_commit<true>(drain, 0x1);
-                mbar_wait_bounded(drain, 0);
+            // After a failed wait: both CTAs' copies count on the even CTA's barriers.
+            if (lane == 0 && !ok && rank == 0) {
+                for (uint32_t q = issued > STAGES ? issued - STAGES : 0; q < issued; ++q)
+                    if (!mbar_wait_bounded(&full[q % STAGES], (q / STAGES) & 1)) break;
             }
             __syncwarp();
-        }
-    } else if (warp < WARP_EPI0) {
-        const int sw_id = warp - WARP_SCALE;           // takes the blocks whose `it` is this modulo SCALE_WARPS
-        float* mine = raw + sw_id * AHEAD * (4 + NBK) * 32 + lane;
-        for (int t = cid; ok && tiles.find(g, lane, t, tl); t += ncl) {
-            // Rows and columns past the ends take the last one's scale; they are not stored.
-            const float* sa[4];
-            const float* sw[NBK];
-            #pragma unroll
-            for (int i = 0; i < 4; ++i) sa[i] = g.sa + min(tl.m0 + (int)rank * BM + 32 * i + lane, tl.r1 - 1);
-            #pragma unroll
-            for (int i = 0; i < NBK; ++i)
-                sw[i] = g.sw + tl.e * g.sw_stride + min(tl.n0 + i * fp8::BLOCK, g.N - 1) / fp8::BLOCK;
-            // Every lane copies what it needs itself, so only its own copies are waited for.
-            auto load = [&](int kb) {
-                if (kb < nk) {
-                    float* d = mine + (kb / SCALE_WARPS % AHEAD) * (4 + NBK) * 32;
-                    #pragma unroll
-                    for (int i = 0; i < 4; ++i) cp_async4(d + 32 * i, sa[i] + kb * g.ldsa);
-                    #pragma unroll
-                    for (int i = 0; i < NBK; ++i) cp_async4(d + 32 * (4 + i), sw[i] + kb * g.ldsw);
+        } else if (warp == WARP_MMA) {
+            if (rank == 0) {
+                // Stages lie 16-byte units apart in the descriptor's address field
+                // (a shared-memory address never carries out of it).
+                const uint64_t adesc = umma_desc_sw128(smem_u32(ring));
+                bool ready = false;                        // the next block's stage and accumulator
+                for (int t = cid; ok && tiles.find(g, lane, t, tl); t += ncl) {
+                    for (int kb = 0; kb < nk; ++kb, ++it) {
+                        const uint32_t s = it % STAGES, b = it % NBUF;
+                        const uint64_t da = adesc + (uint64_t)(s * (C::STAGE >> 4)), dw = da + (A_BYTES >> 4);
+                        ok = ready || (f8_wait_all(&full[s], (it / STAGES) & 1, abort_flag) &&
+                                       (it < NBUF || f8_wait_all(&tempty[b], ((it / NBUF) - 1) & 1, abort_flag)));
+                        if (!ok) break;
+                        tc_fence_after();
+                        const uint32_t nx = it + 1;
+                        const bool f = mbar_test(&full[nx % STAGES], (nx / STAGES) & 1);
+                        const bool e = nx < NBUF || mbar_test(&tempty[nx % NBUF], ((nx / NBUF) - 1) & 1);
+                        if (elect_one()) {
+                            #pragma unroll
+                            for (int kk = 0; kk < 4; ++kk)
+                                mma_f8<2>(tmem_base + b * BN, da + kk * 2, dw + kk * 2, f8_idesc(2 * BM, BN),
+                                          kk != 0 ? 1u : 0u);
+                            f4_commit<true>(&tfull[b], 0x3);
+                            f4_commit<true>(&empty[s], 0x3);
+                        }
+                        ready = __all_sync(0xffffffffu, f && e);
+                    }
                 }
-                cp_async_commit();
-            };
-            const uint32_t it0 = it;
-            const int first = (int)((uint32_t)(sw_id - (int)it0) % SCALE_WARPS);
-            #pragma unroll
-            for (int i = 0; i < AHEAD - 1; ++i) load(first + i * SCALE_WARPS);
-            for (int kb = first; kb < nk; kb += SCALE_WARPS) {
-                it = it0 + kb;
-                const uint32_t b = it % NBUF;
-                load(kb + (AHEAD - 1) * SCALE_WARPS);
-                cp_async_wait<AHEAD - 1>();
-                // The accumulator's previous use is committed: its barrier can
-                // take this block's arrival, and the epilogue is done with the
-                // block 2 NBUF before this one (the MMAs had waited for it).
-                ok = it < NBUF || f8_wait_all(&tfull[b], ((it / NBUF) - 1) & 1, abort_flag);
-                if (!ok) break;
-                const float* d = mine + (kb / SCALE_WARPS % AHEAD) * (4 + NBK) * 32;
-                float* p = prod + (it % (2 * NBUF)) * NBK * BM + lane;
-                #pragma unroll
-                for (int n = 0; n < NBK; ++n) {
-                    const float w = d[32 * (4 + n)];
-                    #pragma unroll
-                    for (int i = 0; i < 4; ++i) p[n * BM + 32 * i] = d[32 * i] * w;
+                if (elect_one()) {
+                    f4_commit<true>(drain, 0x1);
+                    mbar_wait_bounded(drain, 0);
                 }
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&tfull[b]);
             }
-            it = it0 + nk;
+        } else {
+            const int sw_id = warp - WARP_SCALE;           // takes the blocks whose `it` is this modulo SCALE_WARPS
+            float* mine = raw + sw_id * AHEAD * (4 + NBK) * 32 + lane;
+            for (int t = cid; ok && tiles.find(g, lane, t, tl); t += ncl) {
+                // Rows and columns past the ends take the last one's scale; they are not stored.
+                const float* sa[4];
+                const float* sw[NBK];
+                #pragma unroll
+                for (int i = 0; i < 4; ++i) sa[i] = g.sa + min(tl.m0 + (int)rank * BM + 32 * i + lane, tl.r1 - 1);
+                #pragma unroll
+                for (int i = 0; i < NBK; ++i)
+                    sw[i] = g.sw + tl.e * g.sw_stride + min(tl.n0 + i * fp8::BLOCK, g.N - 1) / fp8::BLOCK;
+                // Every lane copies what it needs itself, so only its own copies are waited for.
+                auto load = [&](int kb) {
+                    if (kb < nk) {
+                        float* d = mine + (kb / SCALE_WARPS % AHEAD) * (4 + NBK) * 32;
+                        #pragma unroll
+                        for (int i = 0; i < 4; ++i) cp_async4(d + 32 * i, sa[i] + kb * g.ldsa);
+                        #pragma unroll
+                        for (int i = 0; i < NBK; ++i) cp_async4(d + 32 * (4 + i), sw[i] + kb * g.ldsw);
+                    }
+                    cp_async_commit();
+                };
+                const uint32_t it0 = it;
+                const int first = (int)((uint32_t)(sw_id - (int)it0) % SCALE_WARPS);
+                #pragma unroll
+                for (int i = 0; i < AHEAD - 1; ++i) load(first + i * SCALE_WARPS);
+                for (int kb = first; kb < nk; kb += SCALE_WARPS) {
+                    it = it0 + kb;
+                    const uint32_t b = it % NBUF;
+                    load(kb + (AHEAD - 1) * SCALE_WARPS);
+                    cp_async_wait<AHEAD - 1>();
+                    // The accumulator's previous use is committed: its barrier can
+                    // take this block's arrival, and the epilogue is done with the
+                    // block 2 NBUF before this one (the MMAs had waited for it).
+                    ok = it < NBUF || f8_wait_all(&tfull[b], ((it / NBUF) - 1) & 1, abort_flag);
+                    if (!ok) break;
+                    const float* d = mine + (kb / SCALE_WARPS % AHEAD) * (4 + NBK) * 32;
+                    float* p = prod + (it % (2 * NBUF)) * NBK * BM + lane;
+                    #pragma unroll
+                    for (int n = 0; n < NBK; ++n) {
+                        const float w = d[32 * (4 + n)];
+                        #pragma unroll
+                        for (int i = 0; i < 4; ++i) p[n * BM + 32 * i] = d[32 * i] * w;
+                    }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&tfull[b]);
+                }
+                it = it0 + nk;
+            }
         }
-    } else if (warp >= WARP_EPI0) {
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
         const int quad = warp & 3, part = (warp - WARP_EPI0) >> 2;
         uint8_t* stage = oring + (warp - WARP_EPI0) * OUT_BLOCK;
         const uint32_t hand_back = mapa_shared(smem_u32(tempty), 0);
@@ -759,19 +791,27 @@ fp8_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
                 const float f = sp[(it % (2 * NBUF)) * NBK * BM];
                 const float2 s = make_float2(f, f);
                 bool next = false;
+                // The load of the next 32 columns runs beside the sums of these.
+                const uint32_t t0 = tq + b * BN;
+                uint32_t r[2][32];
+                tmem_ld32_start(t0, r[0]);
                 #pragma unroll
-                for (int c = 0; c < CW; c += 16) {
-                    uint32_t r[16];
-                    tmem_ld16_sync(tq + b * BN + c, r);
-                    if (c + 32 == CW) next = mbar_test(&tfull[(it + 1) % NBUF], ((it + 1) / NBUF) & 1);
+                for (int c = 0; c < CW; c += 32) {
+                    uint32_t(&v)[32] = r[(c / 32) & 1];
+                    tmem_ld32_wait(v);
+                    if (c + 32 < CW) {
+                        tmem_ld32_start(t0 + c + 32, r[(c / 32 + 1) & 1]);
+                    } else {
+                        // Everything has been read and the scale is used: nothing of
+                        // this block is touched after the arrival.
+                        tc_fence_before();
+                        if (elect_one()) mbar_arrive_relaxed(hand_back + b * 8);
+                        next = mbar_test(&tfull[(it + 1) % NBUF], ((it + 1) / NBUF) & 1);
+                    }
                     #pragma unroll
-                    for (int j = 0; j < 16; j += 2)
-                        scale_add2(acc[(c + j) / 2], make_float2(__uint_as_float(r[j]), __uint_as_float(r[j + 1])), s);
+                    for (int j = 0; j < 32; j += 2)
+                        scale_add2(acc[(c + j) / 2], make_float2(__uint_as_float(v[j]), __uint_as_float(v[j + 1])), s);
                 }
-                tc_fence_before();
-                // The loads have completed (wait::ld) and the scale was used: nothing
-                // of this block is read after the arrival.
-                if (elect_one()) mbar_arrive_relaxed(hand_back + b * 8);
                 ready = __all_sync(0xffffffffu, next);
             }
             if (!ok) break;
