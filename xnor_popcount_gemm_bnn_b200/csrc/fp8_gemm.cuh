@@ -171,12 +171,16 @@ __device__ __forceinline__ void scale_add2(float2& acc, float2 t, float2 s) {
         : "l"(reinterpret_cast<unsigned long long&>(t)), "l"(reinterpret_cast<unsigned long long&>(s)));
 }
 
-__device__ __forceinline__ float4 ld_shared_cluster_v4(uint32_t addr) {
+// 16 bytes of the cluster's shared memory; zeros where `on` is 0.
+__device__ __forceinline__ float4 ld_shared_cluster_v4_if(uint32_t addr, int on) {
     float4 v;
-    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-                 : "r"(addr)
-                 : "memory");
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %5, 0;\n\t"
+        "mov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\tmov.b32 %2, 0;\n\tmov.b32 %3, 0;\n\t"
+        "@p ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];\n\t}"
+        : "=&f"(v.x), "=&f"(v.y), "=&f"(v.z), "=&f"(v.w)
+        : "r"(addr), "r"(on)
+        : "memory");
     return v;
 }
 __device__ __forceinline__ uint32_t mapa_shared(uint32_t addr, uint32_t rank) {
@@ -231,6 +235,52 @@ static_assert(SMALLEST <= Cfg<16, true>::SHARE && SMALLEST <= Cfg<32, true>::SHA
                   Cfg<128, true>::SHARE + SMALLEST > SMEM_SM,
               "tensor memory of the CTAs that share an SM");
 }  // namespace f8s
+
+// The sums of S CTAs: parts[column][128] fp32 at the same shared-memory offset
+// in each.  Rank q adds the columns q, q + S, ... in rank order; a warp takes
+// whole columns, four rows of weights per lane, and several of them at a time,
+// since every remote load takes about half a microsecond.
+struct Fp8Parts {
+    uint32_t parts;
+    int rank, warp, warps, cols, m0, n0, vec_out;
+};
+template <int S, typename T>
+__device__ __forceinline__ void add_parts(const Fp8Parts& p, const Fp8Gemm& g, int lane) {
+    constexpr int C = 16 / S;                    // columns whose loads are in flight together
+    const int step = S * p.warps, n = p.n0 + 4 * lane;
+    for (int c0 = p.rank + p.warp * S; c0 < p.cols; c0 += C * step) {
+        float4 v[C][S];
+        #pragma unroll
+        for (int i = 0; i < C; ++i) {
+            const uint32_t at = p.parts + ((c0 + i * step) * f8s::BN + 4 * lane) * 4;
+            const int on = c0 + i * step < p.cols ? 1 : 0;
+            #pragma unroll
+            for (int r = 0; r < S; ++r) v[i][r] = ld_shared_cluster_v4_if(mapa_shared(at, r), on);
+        }
+        #pragma unroll
+        for (int i = 0; i < C; ++i) {
+            const int c = c0 + i * step;
+            if (c >= p.cols) break;
+            float4 y = v[i][0];
+            #pragma unroll
+            for (int r = 1; r < S; ++r) {
+                y.x += v[i][r].x;
+                y.y += v[i][r].y;
+                y.z += v[i][r].z;
+                y.w += v[i][r].w;
+            }
+            T* out = static_cast<T*>(g.out) + (int64_t)(p.m0 + c) * g.ldo + n;
+            if (p.vec_out && n + 4 <= g.N) {
+                store4(out, y);
+            } else {
+                if (n < g.N) out[0] = fp8_out<T>(y.x);
+                if (n + 1 < g.N) out[1] = fp8_out<T>(y.y);
+                if (n + 2 < g.N) out[2] = fp8_out<T>(y.z);
+                if (n + 3 < g.N) out[3] = fp8_out<T>(y.w);
+            }
+        }
+    }
+}
 
 // grid: (tiles of 128 weight rows x E) * S CTAs in clusters of S, y over chunks
 // of NT rows (a group's chunks are walked in steps of gridDim.y).  Cluster
@@ -302,6 +352,7 @@ fp8_gemm_split_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_cons
     uint32_t it = 0;                          // K blocks this role has handled, over all chunks
     uint32_t issued = 0;
     bool ok = true;
+    bool ready = false;                       // what this role waits for is there for its next block
     for (int m0 = rows.x + (int)blockIdx.y * NT; m0 < rows.y; m0 += (int)gridDim.y * NT) {
         if (warp == WARP_PRODUCER) {
             for (int kb = kb0; ok && kb < kb1; ++kb, ++it) {
@@ -324,10 +375,13 @@ fp8_gemm_split_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_cons
             for (int kb = kb0; ok && kb < kb1; ++kb, ++it) {
                 const uint32_t s = it % STAGES, b = it % NBUF;
                 const uint64_t dw = wdesc + (uint64_t)(s * (C::STAGE >> 4)), da = dw + (W_BYTES >> 4);
-                ok = f8_wait_all(&full[s], (it / STAGES) & 1, abort_flag) &&
-                     (it < NBUF || f8_wait_all(&tempty[b], ((it / NBUF) - 1) & 1, abort_flag));
+                ok = ready || (f8_wait_all(&full[s], (it / STAGES) & 1, abort_flag) &&
+                               (it < NBUF || f8_wait_all(&tempty[b], ((it / NBUF) - 1) & 1, abort_flag)));
                 if (!ok) break;
                 tc_fence_after();
+                const uint32_t nx = it + 1;
+                const bool fn = mbar_test(&full[nx % STAGES], (nx / STAGES) & 1);
+                const bool en = nx < NBUF || mbar_test(&tempty[nx % NBUF], ((nx / NBUF) - 1) & 1);
                 if (elect_one()) {
                     #pragma unroll
                     for (int kk = 0; kk < 4; ++kk)
@@ -335,7 +389,7 @@ fp8_gemm_split_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_cons
                     mma_commit(&tfull[b]);
                     mma_commit(&empty[s]);
                 }
-                __syncwarp();
+                ready = __all_sync(0xffffffffu, fn && en);
             }
         } else if (warp == WARP_SCALE) {
             const float* sa = g.sa + m0 + lane;
@@ -379,22 +433,22 @@ fp8_gemm_split_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_cons
             const int quad = warp & 3, part = (warp - WARP_EPI0) >> 2;
             const int cols = min(NT, rows.y - m0);
             const uint32_t tq = tmem_base + ((uint32_t)(32 * quad) << 16) + part * CW;
-            constexpr int CH = CW < 32 ? CW : 32;           // columns per load
+            constexpr int CH = 16;                          // columns per load
             float2 acc[CW / 2];
             #pragma unroll
             for (int c = 0; c < CW / 2; ++c) acc[c] = make_float2(0.0f, 0.0f);
             #pragma unroll 1
             for (int kb = kb0; ok && kb < kb1; ++kb, ++it) {
                 const uint32_t b = it % NBUF;
-                ok = f8_wait_all(&tfull[b], (it / NBUF) & 1, abort_flag);
+                ok = ready || f8_wait_all(&tfull[b], (it / NBUF) & 1, abort_flag);
                 if (!ok) break;
                 tc_fence_after();
+                const bool next = mbar_test(&tfull[(it + 1) % NBUF], ((it + 1) / NBUF) & 1);
                 const float* s = prod + (it % (2 * NBUF)) * NT + part * CW;
                 #pragma unroll
                 for (int c = 0; c < CW; c += CH) {
                     uint32_t r[CH];
-                    if constexpr (CH == 16) tmem_ld16_sync(tq + b * NT + c, r);
-                    else tmem_ld32_sync(tq + b * NT + c, r);
+                    tmem_ld16_sync(tq + b * NT + c, r);
                     #pragma unroll
                     for (int j = 0; j < CH; j += 4) {
                         const float4 f = *reinterpret_cast<const float4*>(s + c + j);
@@ -405,7 +459,7 @@ fp8_gemm_split_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_cons
                     }
                 }
                 tc_fence_before();
-                __syncwarp();                       // every lane has used its scales
+                ready = __all_sync(0xffffffffu, next);   // and every lane has used its scales
                 if (elect_one()) mbar_arrive(&tempty[b]);
             }
             const int n = 32 * quad + lane;
@@ -431,31 +485,16 @@ fp8_gemm_split_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_cons
             __syncwarp();
             cluster_sync_all();
             if (warp >= WARP_EPI0) {
-                // A warp takes whole columns, four rows of weights per lane.
-                const int n = n0 + 4 * lane, cols = min(NT, rows.y - m0);
-                for (int c = rank + (warp - WARP_EPI0) * S; c < cols; c += 4 * C::PARTS * S) {
-                    const uint32_t at = smem_u32(ring) + (c * BN + 4 * lane) * 4;
-                    float4 v[MAX_SPLIT];
-                    #pragma unroll
-                    for (int r = 0; r < MAX_SPLIT; ++r) v[r] = ld_shared_cluster_v4(mapa_shared(at, min(r, S - 1)));
-                    float4 y = v[0];
-                    #pragma unroll
-                    for (int r = 1; r < MAX_SPLIT; ++r) {
-                        y.x += r < S ? v[r].x : 0.0f;
-                        y.y += r < S ? v[r].y : 0.0f;
-                        y.z += r < S ? v[r].z : 0.0f;
-                        y.w += r < S ? v[r].w : 0.0f;
-                    }
-                    T* out = static_cast<T*>(g.out) + (int64_t)(m0 + c) * g.ldo + n;
-                    if (!ok) continue;
-                    if (vec_out && n + 4 <= g.N) {
-                        store4(out, y);
-                    } else {
-                        if (n < g.N) out[0] = fp8_out<T>(y.x);
-                        if (n + 1 < g.N) out[1] = fp8_out<T>(y.y);
-                        if (n + 2 < g.N) out[2] = fp8_out<T>(y.z);
-                        if (n + 3 < g.N) out[3] = fp8_out<T>(y.w);
-                    }
+                const int cols = ok ? min(NT, rows.y - m0) : 0;
+                const Fp8Parts to{smem_u32(ring), rank, warp - WARP_EPI0, 4 * C::PARTS, cols, m0, n0, vec_out};
+                switch (S) {
+                    case 2: add_parts<2, T>(to, g, lane); break;
+                    case 3: add_parts<3, T>(to, g, lane); break;
+                    case 4: add_parts<4, T>(to, g, lane); break;
+                    case 5: add_parts<5, T>(to, g, lane); break;
+                    case 6: add_parts<6, T>(to, g, lane); break;
+                    case 7: add_parts<7, T>(to, g, lane); break;
+                    default: add_parts<8, T>(to, g, lane); break;
                 }
                 // Ordered before the next chunk's copies into the ring.
                 fence_proxy_async_shared();
