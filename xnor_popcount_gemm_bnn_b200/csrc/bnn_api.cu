@@ -1846,31 +1846,31 @@ int fp8_split(int64_t tiles, int64_t slots, int64_t nk) {
 }
 
 template <int NT, bool DEEP, typename T>
-bnn_status launch_fp8_split_as(const CUtensorMap& tmA, const CUtensorMap& tmW, const bnn::Fp8Gemm& g, int64_t chunks,
+bnn_status launch_fp8_split_as(const CUtensorMap& tmA, const CUtensorMap& tmW, const bnn::Fp8Gemm& g,
                                int64_t tiles_n, int S, cudaStream_t stream) {
     using C = bnn::f8s::Cfg<NT, DEEP>;
     const int vec = aligned(g.out, 4 * sizeof(T)) && g.ldo % 4 == 0 ? 1 : 0;
     return launch_clusters(bnn::fp8_gemm_split_kernel<NT, DEEP, T>,
-                           dim3((unsigned)(tiles_n * g.E * S), (unsigned)chunks), C::THREADS, C::SMEM_BYTES, S, stream,
+                           dim3((unsigned)(tiles_n * g.E * S)), C::THREADS, C::SMEM_BYTES, S, stream,
                            tmA, tmW, g, (int)tiles_n, S, vec);
 }
 
 template <int NT, typename T>
-bnn_status launch_fp8_split(const Fp8Operands& o, const bnn::Fp8Gemm& g, int64_t chunks, cudaStream_t stream) {
+bnn_status launch_fp8_split(const Fp8Operands& o, const bnn::Fp8Gemm& g, cudaStream_t stream) {
     CUtensorMap tmA, tmW;
     if (!encode_fp8_map(&tmA, o.A, g.K, g.R, o.lda, 0, 0, NT) ||
         !encode_fp8_map(&tmW, o.W, g.K, g.N, o.ldw, g.E, o.w_stride, bnn::f8s::BN))
         return BNN_ERR_CUDA;
     const int64_t tiles_n = ceil_div(g.N, bnn::f8s::BN), nk = ceil_div(g.K, bnn::fp8::BLOCK);
-    const int S = fp8_split(tiles_n * g.E * chunks, (int64_t)bnn::f8s::Cfg<NT, true>::PER_SM * sm_count(), nk);
+    const int S = fp8_split(tiles_n * g.E, (int64_t)bnn::f8s::Cfg<NT, true>::PER_SM * sm_count(), nk);
     if constexpr (NT == 16) {
         // A short stream per CTA is bound by the launch: the shallow ring
         // lets the next launch set up beside it (11008 x 4096, 11 blocks per
         // CTA: 10.7 us against 11.5).  A long one by memory: the deep ring (64
         // experts of 2048 x 4096, 32 blocks: 68 us against 82).
-        if (ceil_div(nk, S) <= 16) return launch_fp8_split_as<NT, false, T>(tmA, tmW, g, chunks, tiles_n, S, stream);
+        if (ceil_div(nk, S) <= 16) return launch_fp8_split_as<NT, false, T>(tmA, tmW, g, tiles_n, S, stream);
     }
-    return launch_fp8_split_as<NT, true, T>(tmA, tmW, g, chunks, tiles_n, S, stream);
+    return launch_fp8_split_as<NT, true, T>(tmA, tmW, g, tiles_n, S, stream);
 }
 
 template <int BN, typename T>
@@ -1895,13 +1895,19 @@ bnn_status launch_fp8_gemm_as(const Fp8Operands& o, const bnn::Fp8Gemm& g, cudaS
     const bool grouped = g.offsets != nullptr;
     if (ceil_div(g.N, 128) * g.E > (1 << 27) || (ceil_div(g.R, 256) + g.E) * ceil_div(g.N, 128) > (1 << 30))
         return BNN_ERR_UNSUPPORTED;
-    if (rows <= 128) {
-        const int64_t chunks = 1;
-        if (rows <= 16) return launch_fp8_split<16, T>(o, g, chunks, stream);
-        if (rows <= 32) return launch_fp8_split<32, T>(o, g, chunks, stream);
-        if (rows <= 64) return launch_fp8_split<64, T>(o, g, chunks, stream);
-        return launch_fp8_split<128, T>(o, g, chunks, stream);
-    }
+    // Rows of A per MMA of the split kernel: all of them where they are known;
+    // groups are uneven, and one with more rows than that reads its weights
+    // again, so twice the average and more, up to where the pair kernel is
+    // quicker although its tiles have 256 rows.  Measured, us (2048 x 4096
+    // weights), 16 / 32 / 64 / pair:
+    //   64 experts of 4 rows 82 / 85 / 93 / 134, of 16 rows 120 / 93 / 99 / 142;
+    //   32 experts of 16 rows 72 / 57 / 50 / 82, of 32 rows 121 / 77 / 62 / 78,
+    //   of 64 rows 219 / 126 / 89 / 78.
+    // Dense, 11008 x 4096: 128 rows split 22, pair 21; 4096 x 11008: 16 and 24.
+    if (rows <= (grouped ? 6 : 16)) return launch_fp8_split<16, T>(o, g, stream);
+    if (rows <= (grouped ? 14 : 32)) return launch_fp8_split<32, T>(o, g, stream);
+    if (rows <= (grouped ? 48 : 64)) return launch_fp8_split<64, T>(o, g, stream);
+    if (!grouped && rows <= 128) return launch_fp8_split<128, T>(o, g, stream);
     const int64_t tiles_m = grouped ? ceil_div(g.R, 256) + g.E / 2 : ceil_div(g.R, 256);
     const int64_t t256 = tiles_m * ceil_div(g.N, 256), t128 = tiles_m * ceil_div(g.N, 128);
     if (ceil_div(t256, pairs) * 2 <= ceil_div(t128, pairs)) return launch_fp8_pair<256, T>(o, g, t256, pairs, stream);

@@ -282,9 +282,8 @@ __device__ __forceinline__ void add_parts(const Fp8Parts& p, const Fp8Gemm& g, i
     }
 }
 
-// grid: (tiles of 128 weight rows x E) * S CTAs in clusters of S, y over chunks
-// of NT rows (a group's chunks are walked in steps of gridDim.y).  Cluster
-// rank r takes K blocks [r nk / S, (r + 1) nk / S).
+// grid: (tiles of 128 weight rows x E) * S CTAs in clusters of S; a group's
+// rows are walked NT at a time.  Cluster rank r takes K blocks [r nk / S, (r + 1) nk / S).
 //  warp 0     producer: TMA of 128 weight rows and NT rows of A per K block.
 //  warp 1     issues the block's four MMAs (M = 128, N = NT) and commits them
 //             to the accumulator and to the stage.
@@ -353,7 +352,7 @@ fp8_gemm_split_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_cons
     uint32_t issued = 0;
     bool ok = true;
     bool ready = false;                       // what this role waits for is there for its next block
-    for (int m0 = rows.x + (int)blockIdx.y * NT; m0 < rows.y; m0 += (int)gridDim.y * NT) {
+    for (int m0 = rows.x; m0 < rows.y; m0 += NT) {
         if (warp == WARP_PRODUCER) {
             for (int kb = kb0; ok && kb < kb1; ++kb, ++it) {
                 const uint32_t s = it % STAGES;
