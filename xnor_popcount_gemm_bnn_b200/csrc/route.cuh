@@ -245,16 +245,25 @@ __device__ __forceinline__ void sort_keys(uint32_t (&key)[NI], uint32_t (&at)[NI
 // does not settle -- groups on the border, a softmax with a bias, scores that
 // underflow -- goes to route_exact().  In fp64 throughout, the exponentials
 // alone would take several times the kernel's time.
-//   Errors: expf 2^-22 relative (2 ulp), the approximate quotient as much, sums
-//   2^-24 each.  Sigmoid: at most 2^-20.6 of the score; softmax: 2^-19 +
-//   |l - max| 2^-24 of it (21 additions for 512 experts), taken for up to 30
-//   below the maximum; the bias' addition 2^-24 of the choice value.
+//   Errors: expf 2^-22 relative (2 ulp), rcp.approx 2^-23 (1 ulp), sums and
+//   products 2^-24 each.  Sigmoid s = 1 / (1 + e): at most 2^-22 + 2^-23 +
+//   2^-24 of it, and in absolute terms s (1 - s) 2^-22 + s (2^-23 + 2^-24) <=
+//   2^-22.  Softmax: 2^-19 + |l - max| 2^-24 of the score (21 additions for 512
+//   experts), taken for up to 30 below the maximum; beside a bias, in absolute
+//   terms, 2^-22 for the exponential, as much for the sum's, 2^-23 + 2^-23 for
+//   the quotient and the rounded sum and e^-1 2^-24 for the argument, of the
+//   largest score.  The bias' addition: 2^-24 of the choice value.
+__device__ __forceinline__ float rcp_approx(float v) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
 template <int NI, typename T>
 __device__ __forceinline__ void route_token(const T* __restrict__ row, const RouteParams& p, int lane, int& my_e,
                                             float& my_w) {
     uint32_t key[NI];
     float top = -CUDART_INF_F, inv = 0.0f, big = 0.0f;         // big: largest |choice value| or score
-    const float rel = p.sigmoid ? 6.3e-7f : 4.0e-6f;
+    const float rel = p.sigmoid ? 4.2e-7f : 4.0e-6f;
     {
         float s[NI];
         load_logits<NI>(row, p, lane, s);
@@ -267,20 +276,28 @@ __device__ __forceinline__ void route_token(const T* __restrict__ row, const Rou
         if (!p.sigmoid) {
             #pragma unroll
             for (int off = 16; off >= 1; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
-            float sum = 0.0f;
             #pragma unroll
-            for (int i = 0; i < NI; ++i) {
-                s[i] = (on >> i) & 1u ? expf(s[i] - top) : 0.0f;
-                sum += s[i];
+            for (int i = 0; i < NI; ++i) s[i] = (on >> i) & 1u ? expf(s[i] - top) : 0.0f;
+            // Beside a bias the sum's error counts too: there it is taken in fp64.
+            if (p.bias != nullptr) {
+                double sum = 0.0;
+                #pragma unroll
+                for (int i = 0; i < NI; ++i) sum += (double)s[i];
+                sum = warp_sum(sum);
+                inv = sum > 0.0 ? rcp_approx((float)sum) : 0.0f;
+            } else {
+                float sum = 0.0f;
+                #pragma unroll
+                for (int i = 0; i < NI; ++i) sum += s[i];
+                #pragma unroll
+                for (int off = 16; off >= 1; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+                inv = sum > 0.0f ? rcp_approx(sum) : 0.0f;
             }
-            #pragma unroll
-            for (int off = 16; off >= 1; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-            inv = sum > 0.0f ? __fdividef(1.0f, sum) : 0.0f;
             #pragma unroll
             for (int i = 0; i < NI; ++i) s[i] *= inv;
         } else {
             #pragma unroll
-            for (int i = 0; i < NI; ++i) s[i] = __fdividef(1.0f, 1.0f + expf(-s[i]));
+            for (int i = 0; i < NI; ++i) s[i] = rcp_approx(1.0f + expf(-s[i]));
         }
         #pragma unroll
         for (int i = 0; i < NI; ++i) {
@@ -295,7 +312,8 @@ __device__ __forceinline__ void route_token(const T* __restrict__ row, const Rou
     float slack = 0.0f;                                        // two errors of any choice value
     if (p.bias != nullptr || p.kept < p.groups) {
         big = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(big)));
-        slack = 2.0f * (rel + 1.2e-7f) * big;
+        const float err = p.sigmoid ? 2.4e-7f : p.bias != nullptr ? 7.5e-7f * inv : rel * big;
+        slack = 2.0f * (err + 1.2e-7f * big);
         sure = big < 1e30f;
     }
     if (p.kept < p.groups) {
@@ -420,7 +438,7 @@ __device__ __forceinline__ void route_token(const T* __restrict__ row, const Rou
     }
     const bool mine = lane < p.k && cand >= 0;
     float s = 0.0f;
-    if (mine) s = p.sigmoid ? __fdividef(1.0f, 1.0f + expf(-l)) : expf(l - top) * inv;
+    if (mine) s = p.sigmoid ? rcp_approx(1.0f + expf(-l)) : expf(l - top) * inv;
     sure = sure && !(mine && (s < 1e-30f || (!p.sigmoid && l < top - 30.0f)));
     if (!__all_sync(0xffffffffu, sure)) {
         route_exact<NI>(row, p, lane, my_e, my_w);
