@@ -294,3 +294,115 @@ def test_binding_refuses_wrong_tensors():
             bnn.bnn_fp8_gemm(*bad)
     with pytest.raises(TypeError):
         bnn.bnn_fp8_gemm(A, sa, W, sw, 64, out.half())
+
+
+@pytest.mark.parametrize("dtype,ld,offset,K", [
+    ("bf16", 264, 0, 261), ("bf16", 268, 4, 263), ("bf16", 262, 2, 259), ("bf16", 261, 1, 130), ("bf16", 272, 8, 129),
+    ("fp32", 264, 0, 261), ("fp32", 266, 2, 259), ("fp32", 261, 1, 261), ("fp32", 268, 4, 255), ("fp32", 136, 8, 3)])
+@pytest.mark.parametrize("block_rows", [1, 128])
+@pytest.mark.parametrize("rows", [7, 400])
+def test_pack_rows_that_end_inside_a_vector(rows, dtype, ld, offset, K, block_rows):
+    """Every alignment of the rows with a K that ends inside a load; what follows a row (NaN) is not read into it."""
+    flat = torch.full((rows * ld + offset,), float("nan"), dtype=DT[dtype], device=dev())
+    x = flat.as_strided((rows, K), (ld, 1), offset)
+    x.copy_(make(rows, K, ld + K, dtype).to(dev()))
+    codes = torch.full((rows, bnn.bnn_fp8_ld_bytes(K) + 16), 0x5A, dtype=torch.uint8, device=dev())
+    scales = bnn.empty_fp8_scales(rows, K, block_rows, dev())
+    bnn.bnn_fp8_pack(x, codes, scales, block_rows=block_rows)
+    c, s = ref.fp8_pack(x.float().cpu().numpy(), block_rows)
+    assert np.array_equal(u8(codes)[:, :K], c)
+    assert not u8(codes)[:, K:bnn.bnn_fp8_ld_bytes(K)].any()
+    assert (u8(codes)[:, bnn.bnn_fp8_ld_bytes(K):] == 0x5A).all()
+    assert np.array_equal(scales.cpu().numpy(), s)
+
+
+def test_single_row_and_column_views():
+    """M = 1 and N = 1 as torch hands them over: scales of one column and outputs whose strides say nothing."""
+    K = 300
+    A, W = random_codes(1, K, 1), random_codes(1, K, 2)
+    sa, sw = random_scales(K, 1, 3), random_scales(K, 1, 4)
+    out = torch.empty(1, 1, device=dev())
+    bnn.bnn_fp8_gemm(A.to(dev()), sa.t().contiguous().t().to(dev()), W.to(dev()), sw.t().contiguous().t().to(dev()), K,
+                     out)
+    c64, mag = ref.fp8_gemm(A.numpy(), sa.numpy(), W.numpy(), sw.numpy(), K)
+    check(out, c64, mag, K, "fp32")
+
+
+def test_offsets_past_32_bits():
+    """Rows far apart: element offsets beyond 2^32 in the input of a pack, in codes and in the output of a product."""
+    rows, K, N = 300, 200, 130
+    far = 1 << 24                                          # 300 rows apart by 2^24 elements
+    big = torch.empty(rows * far, dtype=torch.bfloat16, device=dev())
+    x = big.as_strided((rows, K), (far, 1))
+    x.copy_(make(rows, K, 5, "bf16").to(dev()))
+    codes, scales = bnn.empty_fp8(rows, K, dev()), bnn.empty_fp8_scales(rows, K, 1, dev())
+    bnn.bnn_fp8_pack(x, codes, scales)
+    c, s = ref.fp8_pack(x.float().cpu().numpy(), 1)
+    assert np.array_equal(u8(codes)[:, :K], c)
+    W, sw = random_codes(N, K, 2), random_scales(K, 2, 4)
+    for m in (300, 100):
+        spread = big.view(torch.uint8).as_strided((m, 208), (far, 1), 1 << 20)
+        spread.copy_(codes.view(torch.uint8)[:m])
+        out = big.as_strided((m, N), (far, 1), 1 << 22)
+        bnn.bnn_fp8_gemm(spread, scales[:, :m].contiguous(), W.to(dev()), sw.to(dev()), K, out)
+        c64, mag = ref.fp8_gemm(c[:m], s[:, :m], W.numpy(), sw.numpy(), K)
+        check(out, c64, mag, K, "bf16")
+    assert_no_device_error()
+
+
+def test_calls_back_to_back_see_one_another():
+    """Each launch may set up beside the one before it: a chain in which every call reads what the last one wrote."""
+    M, K = 40, 512
+    x = make(M, K, 3, "bf16").to(dev())
+    W = torch.stack([bnn.empty_fp8(K, K, dev()) for _ in range(2)])
+    sw = torch.stack([bnn.empty_fp8_scales(K, K, 128, dev()) for _ in range(2)])
+    for i in range(2):
+        bnn.bnn_fp8_pack((make(K, K, 20 + i) * 0.02).to(dev()), W[i], sw[i], block_rows=128)
+
+    def chain(wait):
+        y = x.clone()
+        codes, scales = bnn.empty_fp8(M, K, dev()), bnn.empty_fp8_scales(M, K, 1, dev())
+        for i in range(24):
+            bnn.bnn_fp8_pack(y, codes, scales)
+            if wait:
+                torch.cuda.synchronize()
+            bnn.bnn_fp8_gemm(codes, scales, W[i % 2], sw[i % 2], K, y)
+            if wait:
+                torch.cuda.synchronize()
+        return y
+
+    want = chain(True)
+    for _ in range(5):
+        assert torch.equal(chain(False).view(torch.int16), want.view(torch.int16))
+
+
+@pytest.mark.parametrize("counts", [[3, 2, 4], [40, 30, 35], [300, 10, 200]])
+def test_two_streams_of_different_kernels(counts):
+    """Grouped and dense products of several widths at once on two streams give what they give alone."""
+    N, K = 260, 900
+    R = sum(counts)
+    A, sa = random_codes(R, K, 1).to(dev()), random_scales(K, R, 2).to(dev())
+    W = torch.stack([random_codes(N, K, 10 + e) for e in range(3)]).to(dev())
+    sw = torch.stack([random_scales(K, 3, 50 + e) for e in range(3)]).to(dev())
+    off = torch.tensor(np.concatenate([[0], np.cumsum(counts)]), dtype=torch.int32, device=dev())
+    sizes = [m for m in (1, 20, 60, 100, 200) if m <= R]
+    sas = [sa[:, :m].contiguous() for m in sizes]
+
+    def all_of(stream, outs):
+        bnn.bnn_fp8_gemm_grouped(A, sa, off, W, sw, K, outs[0], stream=stream)
+        for m, s, o in zip(sizes, sas, outs[1:]):
+            bnn.bnn_fp8_gemm(A[:m], s, W[0], sw[0], K, o, stream=stream)
+
+    new = lambda: [torch.empty(R, N, device=dev())] + [torch.empty(m, N, device=dev()) for m in sizes]
+    want = new()
+    all_of(None, want)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = [new() for _ in range(6)]
+    torch.cuda.synchronize()
+    for i, o in enumerate(got):
+        all_of(streams[i % 2], o)
+    torch.cuda.synchronize()
+    for o in got:
+        assert all(torch.equal(a, b) for a, b in zip(o, want))
+    assert_no_device_error()

@@ -262,3 +262,56 @@ def test_layer_of_experts_captured():
         for name in ("idx", "w", "off", "tok", "slot", "out"):
             assert torch.equal(one[name], two[name]), name
     assert_no_device_error()
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("scale", [1e-6, 1e-3, 30.0])
+@pytest.mark.parametrize("groups", [1, 8])
+def test_route_crowded_and_spread_logits(score, scale, groups):
+    """Logits so near that many tokens are decided beyond fp32, and so far apart that scores saturate."""
+    l = draw(200, 128, 3) * scale
+    bias = draw(1, 128, 4, std=1e-7)[0]
+    check(l, 8, score, n_groups=groups, kept_groups=max(1, groups // 2))
+    check(l, 8, score, bias=bias, n_groups=groups, kept_groups=max(1, groups // 2))
+
+
+def test_route_is_the_same_on_every_run_and_stream():
+    l = draw(3000, 64, 6)
+    first = run(l, 6)
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for stream in (None, s, s, None):
+        again = run(l, 6, stream=stream)
+        torch.cuda.synchronize()
+        assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
+        assert all(torch.equal(first[2][n], again[2][n]) for n in first[2])
+
+
+def test_combine_of_no_rows_and_bad_values():
+    """R = 0 gives zeros; a slot left out counts for nothing even where its weight is NaN."""
+    d = dev()
+    out = torch.full((3, 40), 7.0, device=d)
+    slot = torch.full((3, 2), -1, dtype=torch.int32, device=d)
+    w = torch.full((3, 2), float("nan"), device=d)
+    bnn.bnn_route_combine(torch.empty(0, 40, device=d), slot, w, out)
+    assert (out == 0).all()
+    Y = torch.full((4, 40), float("inf"), device=d)
+    Y[2] = 1.5
+    slot = torch.tensor([[2, 4], [-1, 2], [2, 2]], dtype=torch.int32, device=d)
+    w = torch.tensor([[2.0, float("nan")], [float("inf"), 1.0], [1.0, -1.0]], device=d)
+    bnn.bnn_route_combine(Y, slot, w, out)
+    assert torch.equal(out[:, 0].cpu(), torch.tensor([3.0, 1.5, 0.0]))
+
+
+def test_combine_offsets_past_32_bits():
+    d = dev()
+    far = 1 << 24
+    big = torch.zeros(300 * far, dtype=torch.bfloat16, device=d)
+    Y = big.as_strided((300, 24), (far, 1))
+    Y.copy_(draw(300, 24, 2, "bf16").to(d))
+    slot = torch.tensor([[299, 0], [150, 298]], dtype=torch.int32, device=d)
+    w = torch.tensor([[0.5, 0.25], [1.0, -2.0]], device=d)
+    out = torch.empty(2, 24, device=d)
+    bnn.bnn_route_combine(Y, slot, w, out)
+    want, mag = ref.route_combine(Y.float().cpu().numpy(), slot.cpu().numpy(), w.cpu().numpy())
+    assert (np.abs(out.cpu().numpy() - want) <= 2 * 2.0 ** -24 * mag + 2.0 ** -24 * np.abs(want)).all()
