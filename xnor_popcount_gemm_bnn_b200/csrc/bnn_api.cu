@@ -1827,16 +1827,21 @@ struct Fp8Operands {
     int64_t lda, ldw, w_stride;
 };
 
-// Split of K for `tiles` clusters: as many CTAs as the SMs hold at once
-// (`slots`), at the fewest K blocks that a CTA takes one after the other, plus
-// about four blocks' time to start and to add the parts.  Up to two rounds a
-// begun one counts whole; later ones overlap.
+// Split of K for `tiles` clusters, `slots` CTAs at once.  The time is the larger
+// of the weights' stream (16 KiB per block and tile, 2.6 ns of it) and a CTA's
+// chain of blocks (280 ns each, for every round of CTAs), half of the smaller,
+// which overlaps in part, 1.5 us for each further round and 1 us to add the
+// parts.  Measured at M = 1, us, split 1 / 2 / 3 / 4: 4096 x 4096 11.0 / 7.9 /
+// 6.9 / 6.6; 11008 x 4096 12.1 / 11.8 / 10.5 / 14.7; 22016 x 4096 18.6 / 22.1 /
+// 20.6 / 23.9.
 int fp8_split(int64_t tiles, int64_t slots, int64_t nk) {
     int best = 1;
     double best_cost = 1e300;
     for (int s = 1; s <= bnn::f8s::MAX_SPLIT && s <= nk; ++s) {
-        const double rounds = (double)(tiles * s) / (double)slots;
-        const double cost = (rounds <= 2.0 ? std::ceil(rounds) : rounds + 0.5) * (double)(ceil_div(nk, s) + 4);
+        const double rounds = (double)ceil_div(tiles * s, slots);
+        const double stream = 2.6e-3 * (double)(tiles * nk), chain = 0.28 * rounds * (double)ceil_div(nk, s);
+        const double cost =
+            std::max(stream, chain) + 0.5 * std::min(stream, chain) + 1.5 * (rounds - 1.0) + (s > 1 ? 1.0 : 0.0);
         if (cost < best_cost) {
             best_cost = cost;
             best = s;
@@ -1864,11 +1869,14 @@ bnn_status launch_fp8_split(const Fp8Operands& o, const bnn::Fp8Gemm& g, cudaStr
     const int64_t tiles_n = ceil_div(g.N, bnn::f8s::BN), nk = ceil_div(g.K, bnn::fp8::BLOCK);
     const int S = fp8_split(tiles_n * g.E, (int64_t)bnn::f8s::Cfg<NT, true>::PER_SM * sm_count(), nk);
     if constexpr (NT == 16) {
-        // A short stream per CTA is bound by the launch: the shallow ring
-        // lets the next launch set up beside it (11008 x 4096, 11 blocks per
-        // CTA: 10.7 us against 11.5).  A long one by memory: the deep ring (64
-        // experts of 2048 x 4096, 32 blocks: 68 us against 82).
-        if (ceil_div(nk, S) <= 16) return launch_fp8_split_as<NT, false, T>(tmA, tmW, g, tiles_n, S, stream);
+        // Short streams on SMs with two CTAs each are bound by the launch: the
+        // shallow ring lets the next launch set up beside them (11008 x 4096 in
+        // 258 CTAs of 11 blocks: 10.5 us against 10.9).  Else memory is, and
+        // wants the deep one (64 experts of 2048 x 4096: 68 us against 82; 4096 x
+        // 4096 in 128 CTAs: 6.6 against 7.3).
+        const int64_t ctas = tiles_n * g.E * S;
+        if (ceil_div(nk, S) <= 16 && ctas > sm_count() && ctas <= 2 * (int64_t)sm_count())
+            return launch_fp8_split_as<NT, false, T>(tmA, tmW, g, tiles_n, S, stream);
     }
     return launch_fp8_split_as<NT, true, T>(tmA, tmW, g, tiles_n, S, stream);
 }
@@ -1903,7 +1911,7 @@ bnn_status launch_fp8_gemm_as(const Fp8Operands& o, const bnn::Fp8Gemm& g, cudaS
     //   64 experts of 4 rows 82 / 85 / 93 / 134, of 16 rows 120 / 93 / 99 / 142;
     //   32 experts of 16 rows 72 / 57 / 50 / 82, of 32 rows 121 / 77 / 62 / 78,
     //   of 64 rows 219 / 126 / 89 / 78.
-    // Dense, 11008 x 4096: 128 rows split 22, pair 21; 4096 x 11008: 16 and 24.
+    // Dense, 128 rows: 11008 x 4096 split 18.7, pair 21; 4096 x 11008 16 and 24.
     if (rows <= (grouped ? 6 : 16)) return launch_fp8_split<16, T>(o, g, stream);
     if (rows <= (grouped ? 14 : 32)) return launch_fp8_split<32, T>(o, g, stream);
     if (rows <= (grouped ? 48 : 64)) return launch_fp8_split<64, T>(o, g, stream);
@@ -2026,8 +2034,12 @@ bnn_status launch_route_combine(const void* Y, int64_t R, int64_t N, int64_t ldy
                                slot_row, weights, (int)k, static_cast<O*>(out), ldo);
     };
     constexpr int64_t threads = bnn::kCombineThreads;
-    if (vec) return run(bnn::route_combine_kernel<T, O, V, 1>, threads * V);
-    return run(bnn::route_combine_kernel<T, O, 1, 4>, threads * 4);
+    // Rows in flight: eight, or four where there are no more (4096 tokens of 4
+    // rows of 4096 bf16: 31 us against 32; 256 threads rather than 128: 29.5).
+    if (vec)
+        return k <= 4 ? run(bnn::route_combine_kernel<T, O, V, 1, 4>, threads * V)
+                      : run(bnn::route_combine_kernel<T, O, V, 1, 8>, threads * V);
+    return run(bnn::route_combine_kernel<T, O, 1, 4, 4>, threads * 4);
 }
 
 }  // namespace

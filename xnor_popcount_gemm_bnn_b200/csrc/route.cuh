@@ -684,11 +684,11 @@ __device__ __forceinline__ float ldg_if(const __nv_bfloat16* p, int on) {
 
 // Bound by reading the k rows of a token, each once.  A block takes one token
 // and C pieces of V elements per thread, THREADS * V apart; the lanes hold the
-// token's rows and weights, and the loads of eight rows are in flight
-// together (predicated: a branch would wait for each).  V = 16 bytes of T
+// token's rows and weights, and the loads of J rows are in flight together
+// (predicated: a branch would wait for each).  V = 16 bytes of T
 // where every row of Y and out allows it, else 1.
-constexpr int kCombineThreads = 128;
-template <typename T, typename O, int V, int C>
+constexpr int kCombineThreads = 256;
+template <typename T, typename O, int V, int C, int J>
 __global__ void __launch_bounds__(kCombineThreads)
 route_combine_kernel(const T* __restrict__ Y, int64_t R, int64_t N, int64_t ldy, const int32_t* __restrict__ slot_row,
                      const float* __restrict__ weights, int k, O* __restrict__ out, int64_t ldo) {
@@ -714,7 +714,6 @@ route_combine_kernel(const T* __restrict__ Y, int64_t R, int64_t N, int64_t ldy,
                 w = __ldg(weights + t * k + j0 + lane);
             }
             const int n_j = min(32, k - j0);
-            constexpr int J = V == 1 ? 4 : 8;
             for (int j = 0; j < n_j; j += J) {
                 // Slots past k hold row -1 and weight 0.
                 uint4 q[V == 1 ? 1 : J];
