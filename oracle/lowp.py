@@ -6,8 +6,8 @@ sharing no code with the CUDA path:
 * ``e4m3_values``: the 256 code values from the format (sign, 4 exponent bits
   of bias 7, 3 mantissa bits, no infinities, NaN 0x7F and 0xFF).
 * ``fp8_pack``: s = max(amax / 448, 2^-126) rounded to fp32, code nearest to
-  (x * 448) / amax (x * 2^126 for the least scale), product and quotient each
-  rounded to fp32, ties to the even code.
+  x * 448 / amax (x * 2^126 for the least scale) rounded to fp32, ties to the
+  even code.
 * ``fp8_gemm``: products of the real values in float64, and the sum of the
   magnitudes that bounds the rounding of any order of addition.
 * ``route``, ``route_plan``, ``route_combine``: token by token.
@@ -63,11 +63,9 @@ def fp8_pack(x: np.ndarray, block_rows: int):
             s = np.maximum(np.float32(amax) / np.float32(448.0), np.float32(2.0 ** -126))
             scales[b, i] = s
             with np.errstate(invalid="ignore", over="ignore", under="ignore"):
-                # (a power of two keeps x * 448 in range: it changes no rounding)
                 least = amax < 448.0 * 2.0 ** -126
-                two = 2.0 ** (126 if least else -math.frexp(float(amax))[1])
-                y = (t.astype(np.float64) * (two if least else 448.0 * two)).astype(np.float32)
-                q = (y.astype(np.float64) / (1.0 if least else float(amax) * two)).astype(np.float32)
+                q = t.astype(np.float64) * (2.0 ** 126 if least else 448.0) / (1.0 if least else float(amax))
+                q = q.astype(np.float32)
             c = e4m3_nearest(np.where(np.isfinite(t), q, np.float32(0)))
             c = np.where(np.isfinite(t), c, 0x7F)       # the sign of a NaN code says nothing
             codes[i * block_rows:(i + 1) * block_rows, b * BLOCK:(b + 1) * BLOCK] = c

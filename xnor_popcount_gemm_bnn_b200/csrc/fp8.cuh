@@ -5,8 +5,8 @@
 // (4 exponent bits, 3 mantissa bits, largest value 448, NaN 0x7F, no
 // infinities): s = max(amax / 448, 2^-126) with amax the largest finite |x| of
 // the block, so the largest element lands on 448 and no quotient is larger.
-// The quotient is that of x * 448 by amax, both rounded to fp32 (2^-24 each,
-// the product of a bf16 x none, against the 2^-4 of the code itself).  Blocks are 1 x 128 (activations: one
+// The quotient is that of x * 448 by amax, rounded once to fp32 (2^-24, against
+// the 2^-4 of the code itself).  Blocks are 1 x 128 (activations: one
 // row's 128 consecutive elements of K) or 128 x 128 (weights).  The scale of
 // row block i and K block b is scales[b * ld + i]: a product walks K block by
 // block and then reads consecutive rows' scales together.
@@ -56,14 +56,18 @@ struct Quotient {
         m = least ? 0x1p126f : __uint_as_float((262u - e) << 23 | 0x600000u);
         d = least ? 1.0f : __uint_as_float((b & 0x7FFFFFu) | 0x3F800000u);
     }
-    // Two quotients of y = x m, each rounded once: q = y inv is off by two units
-    // at most, its remainder q d - y is exact in one fused multiply-add, and q -
-    // remainder * inv rounds correctly (Markstein, IBM J. Res. Dev. 34, 1990);
-    // written so that a zero keeps its sign.
+    // Two quotients, each rounded once: q = y inv with y = x m is off by two
+    // units at most, its remainder q d - y is exact in one fused multiply-add,
+    // and q - remainder * inv rounds correctly (Markstein, IBM J. Res. Dev. 34,
+    // 1990); written so that a zero keeps its sign.  EXACT: y has no rounding
+    // (bf16: 8 + 3 bits); else its error joins the remainder.
+    template <bool EXACT>
     __device__ __forceinline__ float2 of(float2 x) const {
         const float2 i2 = make_float2(-inv, -inv);
         const float2 ny = mul2(x, make_float2(-m, -m)), q = mul2(ny, i2);
-        return fma2(fma2(q, make_float2(d, d), ny), i2, q);
+        float2 r = fma2(q, make_float2(d, d), ny);
+        if constexpr (!EXACT) r = fma2(fma2(x, make_float2(m, m), ny), make_float2(-1.0f, -1.0f), r);
+        return fma2(r, i2, q);
     }
 };
 
@@ -148,7 +152,7 @@ struct Elems {
             #pragma unroll
             for (int j = 0; j < 2; ++j) {
                 const float2 v = make_float2(value(4 * i + 2 * j), value(4 * i + 2 * j + 1));
-                float2 q = by.of(v);
+                float2 q = by.of<sizeof(T) == 2>(v);
                 if constexpr (SPECIAL) q = make_float2(fmaf(v.x, 0.0f, q.x), fmaf(v.y, 0.0f, q.y));
                 c[j] = codes2(q);
             }
@@ -225,7 +229,7 @@ struct Narrow {
         float2 q[2];
         #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            q[i] = by.of(make_float2(v[2 * i], v[2 * i + 1]));
+            q[i] = by.of<sizeof(T) == 2>(make_float2(v[2 * i], v[2 * i + 1]));
             if (special) q[i] = make_float2(fmaf(v[2 * i], 0.0f, q[i].x), fmaf(v[2 * i + 1], 0.0f, q[i].y));
         }
         const uint32_t lo = codes2(q[0]), hi = codes2(q[1]);
