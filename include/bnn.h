@@ -755,10 +755,12 @@ bnn_status bnn_fp8_pack(const void* x, bnn_dtype dt, int64_t x_rows, int64_t K, 
  *   W        device [N, ldw] codes, w_scales [ceil(K/128), ld_ws] with a scale
  *            per 128 rows (block_rows 128), ld_ws >= ceil(N / 128).
  *   out      device fp32 or bf16 (out_dt) [M, ld_out], ld_out >= N.
- *   A NaN code makes its row (column) of C NaN and nothing else.
+ *   A NaN code makes its row (column) of C NaN and nothing else.  out does not
+ *   overlap the operands.
  *   M, N >= 0, K >= 1, each below 2^31 - 512.
  *   Errors: INVALID_ARG, ALIGNMENT (A, W not 16-byte aligned, lda / ldw not a
- *   multiple of 16), CUDA. */
+ *   multiple of 16), UNSUPPORTED (a stride of 2^40 bytes, more than 2^30 tiles),
+ *   CUDA. */
 bnn_status bnn_fp8_gemm(const uint8_t* A, int64_t lda, const float* a_scales, int64_t ld_as, const uint8_t* W,
                         int64_t ldw, const float* w_scales, int64_t ld_ws, int64_t M, int64_t N, int64_t K, void* out,
                         bnn_dtype out_dt, int64_t ld_out, bnn_stream_t stream);
@@ -776,7 +778,8 @@ bnn_status bnn_fp8_gemm(const uint8_t* A, int64_t lda, const float* a_scales, in
  *            blocks], as one bnn_fp8_pack of all E * N rows writes it when
  *            N % 128 == 0, has ld_ws = E * N / 128 and ws_stride = N / 128).
  *   R, N, E >= 0, K >= 1; E <= 1024.
- *   Errors: INVALID_ARG, ALIGNMENT, UNSUPPORTED (E > 1024), CUDA. */
+ *   Errors: INVALID_ARG, ALIGNMENT, UNSUPPORTED (E > 1024, and as
+ *   bnn_fp8_gemm), CUDA. */
 bnn_status bnn_fp8_gemm_grouped(const uint8_t* A, int64_t lda, const float* a_scales, int64_t ld_as, int64_t R,
                                 const int32_t* offsets, int64_t E, const uint8_t* W, int64_t ldw, int64_t w_stride,
                                 const float* w_scales, int64_t ld_ws, int64_t ws_stride, int64_t N, int64_t K,
