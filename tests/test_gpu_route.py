@@ -275,6 +275,23 @@ def test_route_crowded_and_spread_logits(score, scale, groups):
     check(l, 8, score, bias=bias, n_groups=groups, kept_groups=max(1, groups // 2))
 
 
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("top", [1, 2])
+@pytest.mark.parametrize("E,G", [(128, 8), (64, 16), (40, 4), (256, 8)])
+def test_route_groups_near_the_border(score, top, E, G):
+    """Groups whose two best experts are clear of the rest, and whose scores are a few steps of fp32 apart."""
+    T, per = 120, E // G
+    l = (draw(T, E, 11) * 0.2 - 3.0).reshape(T, G, per)
+    step = torch.randint(-3, 4, (T, G, 2), generator=torch.Generator().manual_seed(5)) * 2.0 ** -22
+    at = torch.argsort(torch.rand(T, G, per, generator=torch.Generator().manual_seed(6)), dim=2)[:, :, :2]
+    l.scatter_(2, at, torch.tensor([2.0, 1.0]) + step)
+    l[::7, 0] = float("-inf")
+    l = l.reshape(T, E)
+    check(l, 4, score, n_groups=G, kept_groups=G // 2, group_top=top)
+    if score == "sigmoid":
+        check(l, 4, score, bias=draw(1, E, 12, std=1e-7)[0], n_groups=G, kept_groups=G // 2, group_top=top)
+
+
 def test_route_is_the_same_on_every_run_and_stream():
     l = draw(3000, 64, 6)
     first = run(l, 6)

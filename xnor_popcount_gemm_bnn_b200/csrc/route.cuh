@@ -237,14 +237,70 @@ __device__ __forceinline__ void sort_keys(uint32_t (&key)[NI], uint32_t (&at)[NI
     }
 }
 
-// One warp, one token, lane l holding experts l * NI .. l * NI + NI - 1 (the
-// lowest index of equal keys is then the first of the lowest lane).  Scores
+// A choice value in fp64.  (A softmax's common divisor, which changes no order
+// where there is no bias, is left out.)
+template <typename T>
+__device__ __forceinline__ double choice_exact(const T* __restrict__ row, const RouteParams& p, int e, float top) {
+    const double l = (double)logit_of(to_float(row[e]));
+    const double s = p.sigmoid ? 1.0 / (1.0 + exp(-l)) : exp(l - (double)top);
+    return p.bias != nullptr ? s + (double)__ldg(p.bias + e) : s;
+}
+
+// Groups whose scores are too near on the border: each group's two best experts
+// (they have to be certainly its two best) again in fp64, and the groups ranked
+// by that.  Groups of whole lanes, a power of two of them.  True in lane g if
+// group g is kept.
+template <int NI, typename T>
+__device__ __forceinline__ bool groups_exact(const T* __restrict__ row, const RouteParams& p, int lane,
+                                             const uint32_t (&key)[NI], float top, float slack, bool& sure) {
+    const int lanes = p.E / p.groups / NI;
+    uint32_t k1 = 0, k2 = 0, k3 = 0;
+    int e1 = -1, e2 = -1;
+    auto insert = [&](uint32_t q, int e) {
+        if (q > k1) {
+            k3 = k2; k2 = k1; e2 = e1; k1 = q; e1 = e;
+        } else if (q > k2) {
+            k3 = k2; k2 = q; e2 = e;
+        } else {
+            k3 = max(k3, q);
+        }
+    };
+    #pragma unroll
+    for (int i = 0; i < NI; ++i) insert(key[i], lane * NI + i);
+    for (int off = 1; off < lanes; off <<= 1) {
+        const uint32_t o1 = __shfl_xor_sync(0xffffffffu, k1, off), o2 = __shfl_xor_sync(0xffffffffu, k2, off);
+        const uint32_t o3 = __shfl_xor_sync(0xffffffffu, k3, off);
+        const int f1 = __shfl_xor_sync(0xffffffffu, e1, off), f2 = __shfl_xor_sync(0xffffffffu, e2, off);
+        insert(o1, f1);
+        insert(o2, f2);
+        k3 = max(k3, o3);
+    }
+    double v = -CUDART_INF;
+    if (k1 != 0) {
+        v = choice_exact(row, p, e1, top);
+        if (k2 != 0) {
+            const double w = choice_exact(row, p, e2, top);
+            v = p.group_top > 1 ? v + w : fmax(v, w);
+        }
+    }
+    sure = sure && __all_sync(0xffffffffu, k3 == 0 || key_value(k2) - key_value(k3) > slack);
+    const double mine = __shfl_sync(0xffffffffu, v, (lane * lanes) & 31);
+    int rank = 0;
+    for (int g = 0; g < p.groups; ++g) {
+        const double o = __shfl_sync(0xffffffffu, mine, g);
+        rank += (o > mine || (o == mine && g < lane)) ? 1 : 0;
+    }
+    return lane < p.groups && mine > -CUDART_INF && rank < p.kept;
+}
+
+// One warp, one token, lane l holding experts l * NI .. l * NI + NI - 1.  Scores
 // are taken in fp32 and every decision is checked against their errors.
 // Choice values nearer than that (other than the same logit and bias, a tie in
-// any precision) are compared again in fp64, one candidate per lane; what that
-// does not settle -- groups on the border, a softmax with a bias, scores that
-// underflow -- goes to route_exact().  In fp64 throughout, the exponentials
-// alone would take several times the kernel's time.
+// any precision) are compared again in fp64, one candidate per lane, and so are
+// groups on the border, by their two best experts; what that does not settle --
+// a softmax with a bias, scores that underflow -- goes to route_exact().  In
+// fp64 throughout, the exponentials alone would take several times the kernel's
+// time.
 //   Errors: expf 2^-22 relative (2 ulp), rcp.approx 2^-23 (1 ulp), sums and
 //   products 2^-24 each.  Sigmoid s = 1 / (1 + e): at most 2^-22 + 2^-23 +
 //   2^-24 of it, and in absolute terms s (1 - s) 2^-22 + s (2^-23 + 2^-24) <=
@@ -360,10 +416,13 @@ __device__ __forceinline__ void route_token(const T* __restrict__ row, const Rou
             const uint32_t o = __shfl_sync(0xffffffffu, mine, g);
             rank += (o > mine || (o == mine && g < lane)) ? 1 : 0;
         }
-        const bool in = mine != 0 && rank < p.kept;
+        bool in = mine != 0 && rank < p.kept;
         const uint32_t least = __reduce_min_sync(0xffffffffu, in ? mine : 0xFFFFFFFFu);
         const uint32_t next = __reduce_max_sync(0xffffffffu, in ? 0u : mine);
-        if (next != 0) sure = sure && key_value(least) - key_value(next) > 2.0f * slack;
+        if (next != 0 && !(key_value(least) - key_value(next) > 2.0f * slack)) {
+            if (whole && (p.sigmoid || p.bias == nullptr)) in = groups_exact<NI>(row, p, lane, key, top, slack, sure);
+            else sure = false;
+        }
         const unsigned kept = __ballot_sync(0xffffffffu, in);
         if (whole) {                                           // (a lane's experts are one group's)
             if (((kept >> (lane * NI / per)) & 1u) == 0) {
@@ -453,8 +512,9 @@ __device__ __forceinline__ void route_token(const T* __restrict__ row, const Rou
 
 // (Registers limited for occupancy: only route_exact() would take more.)  Bound
 // by instruction latency, about 900 a token and 28 % of the issue slots: 8192
-// tokens, 256 experts 12 us, with groups 14 us, plus up to 6 us when a token goes
-// to route_exact() last.  Everything in fp64 and by shuffles it took 62 us.
+// tokens, 256 experts 12 us, with groups 14 us (21 us with groups on the
+// border left to route_exact(), whose last token the launch waits for).
+// Everything in fp64 and by shuffles it took 62 us.
 template <typename T, int NI>
 __global__ void __launch_bounds__(256, 4) route_topk_kernel(const T* __restrict__ logits, RouteParams p) {
     grid_dependency_wait();
