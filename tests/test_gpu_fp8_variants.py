@@ -1,0 +1,117 @@
+"""The variants of the 8-bit products that only larger calls reach: every ring depth and split of K, groups with more
+rows than the few-rows kernel takes at a time, and CTA pairs with several tiles.
+
+The shapes are those that the launchers' rules send to each variant on 148 SMs.  Every element is compared, within the
+bound of test_gpu_fp8.py, with float64 products of the codes' values on the GPU, and two runs bit for bit."""
+import numpy as np
+import pytest
+import torch
+
+import oracle.lowp as ref
+import xnor_popcount_gemm_bnn_b200 as bnn
+from gpu_util import assert_no_device_error, dev
+
+pytestmark = pytest.mark.gpu
+DT = {"fp32": torch.float32, "bf16": torch.bfloat16}
+BLOCK = 128
+
+
+def codes_of(shape, K, seed):
+    """Codes over the whole range but NaN, garbage in the padding past K."""
+    g = torch.Generator(device=dev()).manual_seed(seed)
+    c = torch.randint(0, 256, (*shape, bnn.bnn_fp8_ld_bytes(K)), generator=g, dtype=torch.uint8, device=dev())
+    c[..., :K][(c[..., :K] & 0x7F) == 0x7F] = 0
+    return c
+
+
+def scales_of(shape, seed):
+    g = torch.Generator(device=dev()).manual_seed(seed)
+    return torch.exp(torch.randn(shape, generator=g, device=dev())) * 0.01
+
+
+def values(codes, scales, K, block_rows):
+    """float64 values of codes [rows, ld] with block-major scales [blocks of K, row blocks]."""
+    table = torch.from_numpy(ref.VALUES).to(dev())
+    rows = codes.shape[0]
+    i, b = torch.arange(rows, device=dev()) // block_rows, torch.arange(K, device=dev()) // BLOCK
+    return table[codes[:, :K].long()] * scales.double()[b[None, :], i[:, None]]
+
+
+def check(out, a, w, K):
+    """|C - C64| <= (128 * 2^-23 + (2 * blocks + 2) * 2^-24) * sum |a w| and half a step of the output type."""
+    c64, mag = a @ w.t(), a.abs() @ w.abs().t()
+    half = torch.finfo(out.dtype).eps / 2
+    blocks = -(-K // BLOCK)
+    tol = (128 * 2.0 ** -23 + (2 * blocks + 2) * 2.0 ** -24) * mag * (1 + half) + half * c64.abs()
+    bad = ~((out.double() - c64).abs() <= tol)
+    assert not bad.any(), (int(bad.sum()), bad.nonzero()[:3].tolist())
+
+
+# rows per MMA and split of K of the few-rows kernel; the shallow ring first (with 3 and 2 parts)
+FEW = [(1, 11008, 4096), (16, 12800, 4096), (9, 300, 896), (5, 300, 640), (10, 300, 900), (20, 12800, 4096),
+       (30, 260, 900), (60, 12600, 4000), (40, 300, 760), (70, 200, 900), (100, 6200, 4000), (128, 4600, 4000),
+       (128, 9400, 4096)]
+# CTA pairs: 256 columns with more than 74 tiles, an odd number of K blocks and a second band of row tiles; 128 columns
+MANY = [(2300, 4000, 610), (2560, 4096, 256), (2500, 2000, 290)]
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("M,N,K", FEW + MANY)
+def test_dense(M, N, K, dtype):
+    A, W = codes_of((M,), K, M + K), codes_of((N,), K, N + K + 1)
+    kb = -(-K // BLOCK)
+    sa, sw = scales_of((kb, M), 5), scales_of((kb, -(-N // BLOCK)), 6)
+    out, again = (torch.full((M, N), float("nan"), dtype=DT[dtype], device=dev()) for _ in range(2))
+    bnn.bnn_fp8_gemm(A, sa, W, sw, K, out)
+    bnn.bnn_fp8_gemm(A, sa, W, sw, K, again)
+    check(out, values(A, sa, K, 1), values(W, sw, K, BLOCK), K)
+    assert torch.equal(out, again)
+    assert_no_device_error()
+
+
+def uneven(E, R, most, seed):
+    """Row counts of E groups, R in all: one of `most` rows, every third group empty, the others uneven."""
+    g = np.random.default_rng(seed)
+    p = g.random(E) * (np.arange(E) % 3 != 1)
+    p[E // 2] = 0
+    c = np.floor(p / p.sum() * (R - most)).astype(np.int64)
+    c[E // 2] = most
+    c[0 if E // 2 else -1] += R - c.sum()
+    return c
+
+
+GROUPED = [  # R, rows of the largest group, N, K, E
+    (200, 70, 260, 300, 40),        # 16 rows at a time, K not split, up to 5 turns of a group
+    (200, 200, 260, 300, 40),       # all rows one group's
+    (200, 70, 260, 2000, 40),       # the shallow ring, 2 parts: the ring is reused after the parts' sums
+    (120, 50, 260, 2000, 20),       # 4 parts
+    (240, 90, 260, 300, 20),        # 32 rows at a time
+    (260, 101, 130, 1300, 20),      # 6 parts
+    (900, 300, 300, 700, 20),       # 64 rows at a time
+    (1300, 333, 140, 900, 30),      # 4 parts
+    (2100, 600, 520, 300, 40),      # pairs of 128 columns, more groups than the tile walk looks at together
+    (2000, 700, 2048, 200, 16),     # pairs of 256 columns
+    (9000, 2500, 1000, 610, 36),    # pairs with several tiles, an odd number of K blocks, two bands in a group
+]
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("R,most,N,K,E", GROUPED)
+def test_grouped(R, most, N, K, E, dtype):
+    first, tail = 3, 5
+    counts = uneven(E, R - first - tail, most, E + R) if most < R else np.eye(E, dtype=np.int64)[E // 2] * (R - first - tail)
+    off = np.concatenate([[0], np.cumsum(counts)]) + first
+    assert off[-1] == R - tail and (counts >= 0).all() and (counts == 0).any()
+    A, W = codes_of((R,), K, 1), codes_of((E, N), K, 2)
+    kb = -(-K // BLOCK)
+    sa, sw = scales_of((kb, R), 3), scales_of((E, kb, -(-N // BLOCK)), 4)
+    offsets = torch.tensor(off, dtype=torch.int32, device=dev())
+    out, again = (torch.full((R, N), 99.0, dtype=DT[dtype], device=dev()) for _ in range(2))
+    bnn.bnn_fp8_gemm_grouped(A, sa, offsets, W, sw, K, out)
+    bnn.bnn_fp8_gemm_grouped(A, sa, offsets, W, sw, K, again)
+    for e in np.nonzero(counts)[0]:
+        r = slice(int(off[e]), int(off[e + 1]))
+        check(out[r], values(A[r], sa[:, r], K, 1), values(W[e], sw[e], K, BLOCK), K)
+    assert (out[:first] == 99.0).all() and (out[R - tail:] == 99.0).all()
+    assert torch.equal(out, again)
+    assert_no_device_error()
