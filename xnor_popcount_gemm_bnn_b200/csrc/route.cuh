@@ -507,7 +507,8 @@ __device__ __forceinline__ void route_token(const T* __restrict__ row, const Rou
     #pragma unroll
     for (int off = 16; off >= 1; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
     my_e = mine ? cand : -1;
-    my_w = (p.renorm ? (sum > 0.0f ? s / sum : 0.0f) : s) * (float)p.scale;
+    // The scale is a double, and may lie outside of fp32 where the weight does not.
+    my_w = (float)((double)(p.renorm ? (sum > 0.0f ? s / sum : 0.0f) : s) * p.scale);
 }
 
 // (Registers limited for occupancy: only route_exact() would take more.)  Bound
