@@ -811,7 +811,8 @@ typedef struct bnn_route_params {
  *   weight_j = score of the j-th, divided by the sum of the k if renormalize,
  *   times scale.
  * Scores and comparisons are in fp64 (a choice is a whole number: fp32 ties
- * would make it depend on rounding); equal values go to the lowest index.  An
+ * would make it depend on rounding), and so are the weights, rounded to fp32
+ * once; equal values go to the lowest index.  An
  * expert whose logit is NaN or -inf, or whose bias is NaN or -inf, is never
  * chosen; a logit of +inf counts as the largest finite fp32.  A token with
  * fewer than k experts to choose from gets index -1 and weight 0 in its last

@@ -1,4 +1,4 @@
-"""The weights of bnn_route against the oracle's fp64 ones: their range."""
+"""The weights of bnn_route against the oracle's fp64 ones: rounded once, and their range."""
 import numpy as np
 import pytest
 import torch
@@ -42,3 +42,21 @@ def test_scale_beyond_fp32(score, renormalize, scale):
     fine = sure & (np.abs(ww) < top)
     assert sure.any() and np.array_equal(gw[over], np.sign(ww[over]) * np.inf)
     assert (np.abs(gw - ww)[fine] <= rel * np.abs(ww[fine]) + 2.0 ** -149).all()
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("renormalize", [False, True])
+@pytest.mark.parametrize("T,E,k,std,groups,with_bias", [
+    (1, 8, 2, 1.5, 1, False), (16, 64, 4, 1.5, 1, True), (40, 64, 6, 8.0, 1, False), (300, 128, 8, 1.5, 8, False),
+    (200, 256, 8, 4.0, 1, True), (100, 257, 7, 8.0, 1, False), (100, 512, 16, 3.0, 16, True),
+    (60, 60, 6, 30.0, 6, False), (60, 40, 40 // 4, 0.01, 1, False)])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_weights_are_rounded_once(T, E, k, std, groups, with_bias, score, renormalize, dtype):
+    """fp64 scores rounded to fp32 at the end: half a step, 2^-24 of the weight (and 2^-150 where it is subnormal),
+    whichever way the choice was settled; 1e-12 covers the fp64 sums of up to 512 terms on both sides."""
+    logits = draw(T, E, T + E, std).to(dtype)
+    bias = draw(1, E, 9, 0.1)[0] if with_bias else None
+    gi, gw, wi, ww = weights(logits, k, score, bias, renormalize=renormalize, scale=1.7, n_groups=groups,
+                             kept_groups=max(1, groups // 2))
+    assert np.array_equal(gi, wi)
+    assert (np.abs(gw - ww) <= (2.0 ** -24 + 1e-12) * np.abs(ww) + 2.0 ** -150).all()
