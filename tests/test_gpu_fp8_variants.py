@@ -115,3 +115,12 @@ def test_grouped(R, most, N, K, E, dtype):
     assert (out[:first] == 99.0).all() and (out[R - tail:] == 99.0).all()
     assert torch.equal(out, again)
     assert_no_device_error()
+
+
+def test_no_experts():
+    """A product with an empty set of experts leaves its outputs as they were."""
+    A, sa, out = codes_of((4,), 64, 1), scales_of((1, 4), 2), torch.full((4, 8), 99.0, device=dev())
+    bnn.bnn_fp8_gemm_grouped(A, sa, torch.zeros(1, dtype=torch.int32, device=dev()), A.new_empty(0, 8, 64),
+                             sa.new_empty(0, 1, 1), 64, out)
+    assert (out == 99.0).all()
+    assert_no_device_error()

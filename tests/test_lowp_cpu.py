@@ -192,3 +192,19 @@ def test_route_combine_refusals():
     assert call(w=FAKE2) == ALN
     assert call(T=0, slot=NULL, w=NULL, out=NULL) == OK
     assert call(N=0, Y=NULL) == OK
+
+
+def test_fp8_gemm_grouped_without_experts():
+    """E = 0 is allowed and launches nothing: the empty arrays W, w_scales and offsets may be NULL, also through the
+    binding's torch tensors of no elements, whose address is 0."""
+    def call(W=NULL, sw=NULL, off=NULL, E=0, N=200, ldsa=8):
+        return L.bnn_fp8_gemm_grouped(FAKE, 208, FAKE, ldsa, 8, off, E, W, 208, 200 * 208, sw, 2, 4, N, 200, FAKE, 1,
+                                      200, NULL)
+    assert call() == OK
+    assert call(W=FAKE) == OK
+    assert call(off=FAKE2) == ALN                           # what is given is still checked
+    assert call(ldsa=7) == INV
+    assert call(E=1) == INV
+    assert call(E=1, W=FAKE, off=FAKE) == INV
+    assert call(E=1, W=FAKE, sw=FAKE) == INV
+    assert torch.empty(0, 200, 208).data_ptr() == 0

@@ -1714,11 +1714,11 @@ constexpr int64_t kMaxDim = INT_MAX - 512;       // tile arithmetic stays within
 
 // Arguments that the dense and the grouped product share.
 bnn_status check_fp8_product(const uint8_t* A, int64_t lda, const float* sa, int64_t ldsa, const uint8_t* W,
-                             int64_t ldw, const float* sw, int64_t ldsw, int64_t M, int64_t N, int64_t K,
+                             int64_t ldw, const float* sw, int64_t ldsw, int64_t M, int64_t N, int64_t K, int64_t E,
                              const void* out, int out_dt, int64_t ldo) {
     if (!real_dtype(out_dt) || M < 0 || N < 0 || K < 1 || M > kMaxDim || N > kMaxDim || K > kMaxDim)
         return BNN_ERR_INVALID_ARG;
-    const bool empty = M == 0 || N == 0;                  // nothing is read or written: no pointer is needed
+    const bool empty = M == 0 || N == 0 || E == 0;        // nothing is read or written: no pointer is needed
     if (!empty && (A == nullptr || sa == nullptr || W == nullptr || sw == nullptr || out == nullptr))
         return BNN_ERR_INVALID_ARG;
     const int64_t ld = bnn_fp8_ld_bytes(K);
@@ -2087,7 +2087,7 @@ bnn_status bnn_fp8_gemm(const uint8_t* A, int64_t lda, const float* a_scales, in
                         int64_t ldw, const float* w_scales, int64_t ld_ws, int64_t M, int64_t N, int64_t K, void* out,
                         bnn_dtype out_dt, int64_t ld_out, bnn_stream_t stream) {
     const bnn_status st =
-        check_fp8_product(A, lda, a_scales, ld_as, W, ldw, w_scales, ld_ws, M, N, K, out, out_dt, ld_out);
+        check_fp8_product(A, lda, a_scales, ld_as, W, ldw, w_scales, ld_ws, M, N, K, 1, out, out_dt, ld_out);
     if (st != BNN_OK) return st;
     if (M == 0 || N == 0) return BNN_OK;
     const bnn::Fp8Gemm g{a_scales, ld_as, w_scales, ld_ws, 0, nullptr, (int)M, 1, (int)N, (int)K, out, ld_out};
@@ -2099,7 +2099,7 @@ bnn_status bnn_fp8_gemm_grouped(const uint8_t* A, int64_t lda, const float* a_sc
                                 const float* w_scales, int64_t ld_ws, int64_t ws_stride, int64_t N, int64_t K,
                                 void* out, bnn_dtype out_dt, int64_t ld_out, bnn_stream_t stream) {
     const bnn_status st =
-        check_fp8_product(A, lda, a_scales, ld_as, W, ldw, w_scales, ld_ws, R, N, K, out, out_dt, ld_out);
+        check_fp8_product(A, lda, a_scales, ld_as, W, ldw, w_scales, ld_ws, R, N, K, E, out, out_dt, ld_out);
     if (st != BNN_OK) return st;
     if (E < 0 || ws_stride < 0 || (offsets == nullptr && E > 0 && R > 0 && N > 0)) return BNN_ERR_INVALID_ARG;
     if (ldw > INT64_MAX / (N + 1) || w_stride < N * ldw) return BNN_ERR_INVALID_ARG;
