@@ -757,6 +757,9 @@ bnn_status bnn_fp8_pack(const void* x, bnn_dtype dt, int64_t x_rows, int64_t K, 
  *   out      device fp32 or bf16 (out_dt) [M, ld_out], ld_out >= N.
  *   A NaN code makes its row (column) of C NaN and nothing else.  out does not
  *   overlap the operands.
+ *   The product sA * sW of two scales is itself one fp32 number, rounded once:
+ *   below 2^-126 it keeps fewer bits (it is a multiple of 2^-149), and from 2^128
+ *   on it is infinite and C infinite or NaN, whatever the codes are.
  *   M, N >= 0, K >= 1, each below 2^31 - 512.
  *   Errors: INVALID_ARG, ALIGNMENT (A, W not 16-byte aligned, lda / ldw not a
  *   multiple of 16), UNSUPPORTED (a stride of 2^40 bytes, more than 2^30 tiles),

@@ -124,3 +124,54 @@ def test_no_experts():
                              sa.new_empty(0, 1, 1), 64, out)
     assert (out == 99.0).all()
     assert_no_device_error()
+
+
+@pytest.mark.parametrize("M", [5, 70, 150])
+@pytest.mark.parametrize("low", [-126, -140, -148])
+def test_small_scale_products(M, low):
+    """Products of scales down to 2^low.  From 2^-126 on the usual bound holds; below it a product is rounded to a
+    multiple of 2^-149, off by 2^-150 at most, times the block's sum; and each block's addition to a sum that may be
+    subnormal is off by 2^-150."""
+    N, K = 140, 500
+    kb = -(-K // BLOCK)
+    A, W = codes_of((M,), K, 1), codes_of((N,), K, 2)
+    sa = (1.0 + scales_of((kb, M), 3).clamp(0, 0.9)) * 2.0 ** (low // 2)
+    sw = (1.0 + scales_of((kb, 2), 4).clamp(0, 0.9)) * 2.0 ** (low - low // 2)
+    out = torch.empty(M, N, device=dev())
+    bnn.bnn_fp8_gemm(A, sa, W, sw, K, out)
+    a, w = values(A, sa, K, 1), values(W, sw, K, BLOCK)
+    one = torch.ones(kb, M, device=dev()), torch.ones(kb, 2, device=dev())
+    inner = values(A, one[0], K, 1).abs() @ values(W, one[1], K, BLOCK).abs().t()
+    c64, mag = a @ w.t(), a.abs() @ w.abs().t()
+    tol = (128 * 2.0 ** -23 + (2 * kb + 2) * 2.0 ** -24) * mag + 2.0 ** -150 * (kb + (inner if low < -126 else 0.0))
+    assert ((out.double() - c64).abs() <= tol).all()
+    assert (out != 0).any()
+    assert_no_device_error()
+
+
+@pytest.mark.parametrize("M", [5, 70, 150])
+def test_large_scale_products(M):
+    """Products of scales up to the largest fp32 number, beside one past it: that row's outputs in those columns are not
+    finite, all others are right."""
+    N, K = 140, 500
+    kb = -(-K // BLOCK)
+    A, W = codes_of((M,), K, 1), codes_of((N,), K, 2)
+    A = torch.where((A & 0x7F) > 0x30, A & 0x87, A)          # |values| of at most 2^-1, so that the sums stay finite
+    W = torch.where((W & 0x7F) > 0x30, W & 0x87, W)
+    sa = torch.full((kb, M), 2.0 ** 60, device=dev())
+    sw = torch.full((kb, 2), 2.0 ** 50, device=dev())
+    sw[1, 1] = 2.0 ** 67
+    sa[1, 3] = 1.5 * 2.0 ** 60
+    sa[1, 2] = 2.0 ** 61
+    out = torch.empty(M, N, device=dev())
+    bnn.bnn_fp8_gemm(A, sa, W, sw, K, out)
+    ok = torch.ones(M, N, dtype=torch.bool, device=dev())
+    ok[2, BLOCK:] = False
+    assert not out[~ok].isfinite().any()
+    a, w = values(A, sa, K, 1), values(W, sw, K, BLOCK)
+    c64, mag = a @ w.t(), a.abs() @ w.abs().t()
+    ok &= mag < 2.0 ** 127
+    assert ok.sum() >= M * BLOCK
+    tol = (128 * 2.0 ** -23 + (2 * kb + 2) * 2.0 ** -24) * mag
+    assert ((out.double() - c64).abs() <= tol)[ok].all()
+    assert_no_device_error()

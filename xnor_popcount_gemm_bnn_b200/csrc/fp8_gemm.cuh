@@ -3,8 +3,11 @@
 //
 // The inner sum of a block is four tcgen05.mma kind::f8f6f4 (K = 32 each) into
 // a fresh fp32 accumulator in tensor memory; the sum over blocks is kept in
-// fp32 registers, C += s * inner, because every block has its own scale.  K
-// tails need no care: the tensor maps end at K, so the copies fill zeros.
+// fp32 registers, C += s * inner, because every block has its own scale.  s =
+// sA sW is rounded to fp32 before it meets the sum (one multiplication per row
+// and block instead of one per element), which limits the scales' range: see
+// bnn_fp8_gemm.  K tails need no care: the tensor maps end at K, so the copies
+// fill zeros.
 //
 // Two kernels share the work:
 //  * fp8_gemm_split_kernel, few rows: the weights are the 128-row operand of
