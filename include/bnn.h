@@ -727,6 +727,8 @@ int64_t bnn_fp8_ld_bytes(int64_t K);
  *   s = max(amax / 448, 2^-126), amax = the largest finite |x| of the block,
  *   code = e4m3(x / s), the quotient being x * 448 / amax rounded once to
  *   fp32 (x * 2^126 where s is 2^-126), the code its nearest, ties to even.
+ *   With dt fp32 a quotient within 2^-21 of a unit of the middle of two fp32
+ *   numbers may be rounded to either of them.
  *   Infinities and NaN become the NaN code 0x7F (or 0xFF) and do not count for amax.
  *   x        device, [x_rows, K] row-major, dtype dt, row stride ld_x >= K
  *            elements.

@@ -87,3 +87,44 @@ def test_rows_of_many_blocks_per_warp(dtype, ld, offset, K, gather):
     assert torch.equal(scales[:, :rows][:, keep], ws[:, keep]) and (scales[:, rows:] == -7.0).all()
     assert (codes[~keep] == 0x5A).all() and (scales[:, :rows][:, ~keep] == -7.0).all()
     assert_no_device_error()
+
+
+def near_middles():
+    """(x, amax), 24-bit integers, whose quotient x * 448 / amax is the middle of two fp32 numbers or very near it, and
+    next to the middle of two codes: T * 2^b - or + half a unit, T odd with five bits."""
+    found = []
+    for T in range(17, 32, 2):
+        for b in range(3, 7):
+            step = 2 ** (20 - b)
+            for m in range(2 ** 23 // step, 2 ** 24 // step):
+                for j in (-2, -1, 0, 1, 2):
+                    for sign in (-1, 1):
+                        amax = m * step + j
+                        n = T * amax * 2 ** b + sign * m
+                        if n % 448 == 0 and 2 ** 23 <= amax < 2 ** 24 and 2 ** 23 <= n // 448 < 2 ** 24:
+                            found.append((n // 448, amax))
+    return found
+
+
+@pytest.mark.parametrize("shift", [0, -60, 80])
+@pytest.mark.parametrize("block_rows", [1, BLOCK])
+def test_fp32_quotients_next_to_a_middle(block_rows, shift):
+    """fp32 quotients that 2^-21 of a unit may send to either neighbour: the code is one of those next to the real
+    quotient, and no farther from it than the nearest by more than the quotient's own rounding, 2^-24 (1 + 2^-20) of it
+    on both sides of the middle."""
+    from fractions import Fraction as F
+    pairs = [p for p in near_middles() if p[0] <= p[1]] + [(10335963, 12582912), (10335963 // 2 * 2, 12582912)]
+    assert len(pairs) > 10
+    rows = len(pairs) * block_rows                            # a pair in a block of its own
+    x = torch.zeros(rows, 40)
+    for i, (v, amax) in enumerate(pairs):
+        x[i * block_rows, :3] = torch.tensor([float(amax), float(v), -float(v)]) * 2.0 ** shift
+    codes, scales = bnn.empty_fp8(rows, 40, dev()), bnn.empty_fp8_scales(rows, 40, block_rows, dev())
+    bnn.bnn_fp8_pack(x.to(dev()), codes, scales, block_rows=block_rows)
+    got = codes.double().cpu()[::block_rows, :3].tolist()
+    positive = [F(v) for v in ref.VALUES[:127].tolist()]
+    for (v, amax), (top, up, down) in zip(pairs, got):
+        q = F(v * 448, amax)
+        best = min(abs(q - c) for c in positive)
+        assert top == 448.0 and down == -up
+        assert abs(q - F(up)) <= best + 2 * q * F(1 + 2 ** -20) / 2 ** 24, (v, amax, up)

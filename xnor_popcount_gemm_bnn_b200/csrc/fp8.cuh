@@ -6,7 +6,7 @@
 // infinities): s = max(amax / 448, 2^-126) with amax the largest finite |x| of
 // the block, so the largest element lands on 448 and no quotient is larger.
 // The quotient is that of x * 448 by amax, rounded once to fp32 (2^-24, against
-// the 2^-4 of the code itself).  Blocks are 1 x 128 (activations: one
+// the 2^-4 of the code itself; see Quotient for fp32 x).  Blocks are 1 x 128 (activations: one
 // row's 128 consecutive elements of K) or 128 x 128 (weights).  The scale of
 // row block i and K block b is scales[b * ld + i]: a product walks K block by
 // block and then reads consecutive rows' scales together.
@@ -56,11 +56,17 @@ struct Quotient {
         m = least ? 0x1p126f : __uint_as_float((262u - e) << 23 | 0x600000u);
         d = least ? 1.0f : __uint_as_float((b & 0x7FFFFFu) | 0x3F800000u);
     }
-    // Two quotients, each rounded once: q = y inv with y = x m is off by two
-    // units at most, its remainder q d - y is exact in one fused multiply-add,
-    // and q - remainder * inv rounds correctly (Markstein, IBM J. Res. Dev. 34,
-    // 1990); written so that a zero keeps its sign.  EXACT: y has no rounding
-    // (bf16: 8 + 3 bits); else its error joins the remainder.
+    // Two quotients: q = y inv with y = x m is off by less than one and a half
+    // units, and q - remainder * inv, the remainder q d - y from one fused
+    // multiply-add, rounds correctly where the remainder is exact (Markstein,
+    // IBM J. Res. Dev. 34, 1990); written so that a zero keeps its sign.
+    // EXACT (bf16): y has 8 + 3 bits and d 8, so y and the remainder are exact,
+    // and no quotient lies within 2^-9 of a unit of the middle of two numbers.
+    // Else y's error joins the remainder, which may take a 25th bit: the
+    // remainder's two roundings and that of inv are 2^-23 of a unit each, and a
+    // quotient that lies within 2^-21 of a unit of the middle of two numbers may
+    // go to either.  (With 27 bits over 24 it can be the middle itself: 10335963 *
+    // 448 / 12582912 = 368 - 2^-16 goes to 368 - 2^-15.)
     template <bool EXACT>
     __device__ __forceinline__ float2 of(float2 x) const {
         const float2 i2 = make_float2(-inv, -inv);
