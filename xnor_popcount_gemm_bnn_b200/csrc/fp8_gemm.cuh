@@ -818,6 +818,7 @@ fp8_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
                 }
                 it = it0 + nk;
             }
+            cp_async_wait<0>();                            // (after a failed wait some are in flight)
         }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
