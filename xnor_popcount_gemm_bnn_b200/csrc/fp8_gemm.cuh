@@ -186,6 +186,11 @@ __device__ __forceinline__ float4 ld_shared_cluster_v4_if(uint32_t addr, int on)
         : "memory");
     return v;
 }
+// Orders the accesses to the cluster's shared memory so far before the
+// asynchronous copies that a barrier lets go after it.
+__device__ __forceinline__ void fence_proxy_async_cluster() {
+    asm volatile("fence.proxy.async.shared::cluster;" ::: "memory");
+}
 __device__ __forceinline__ uint32_t mapa_shared(uint32_t addr, uint32_t rank) {
     uint32_t r;
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
@@ -503,8 +508,9 @@ fp8_gemm_split_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_cons
                     case 7: add_parts<7, T>(to, g, lane); break;
                     default: add_parts<8, T>(to, g, lane); break;
                 }
-                // Ordered before the next chunk's copies into the ring.
-                fence_proxy_async_shared();
+                // Ordered before the next chunk's copies into the ring, which this
+                // CTA's threads have written and the cluster's have read.
+                fence_proxy_async_cluster();
             }
             __syncwarp();
             cluster_sync_all();
