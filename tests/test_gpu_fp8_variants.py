@@ -175,3 +175,21 @@ def test_large_scale_products(M):
     tol = (128 * 2.0 ** -23 + (2 * kb + 2) * 2.0 ** -24) * mag
     assert ((out.double() - c64).abs() <= tol)[ok].all()
     assert_no_device_error()
+
+
+@pytest.mark.parametrize("rows", [2, 60])
+def test_experts_past_32_bits(rows):
+    """Experts' weights and scales more than 2^32 bytes from the first's."""
+    E, N, K = 70, 130, 200
+    far = 1 << 26                                             # 70 experts apart by 2^26 bytes, of either
+    W = torch.empty(E * far, dtype=torch.uint8, device=dev()).as_strided((E, N, 208), (far, 208, 1))
+    sw = torch.empty(E * far // 4, device=dev()).as_strided((E, 2, 2), (far // 4, 2, 1))
+    W.copy_(codes_of((E, N), K, 1))
+    sw.copy_(scales_of((E, 2, 2), 2))
+    A, sa = codes_of((E * rows,), K, 3), scales_of((2, E * rows), 4)
+    out = torch.empty(E * rows, N, device=dev())
+    bnn.bnn_fp8_gemm_grouped(A, sa, torch.arange(0, E * rows + 1, rows, dtype=torch.int32, device=dev()), W, sw, K, out)
+    for e in range(E):
+        r = slice(e * rows, (e + 1) * rows)
+        check(out[r], values(A[r], sa[:, r], K, 1), values(W[e], sw[e], K, BLOCK), K)
+    assert_no_device_error()
