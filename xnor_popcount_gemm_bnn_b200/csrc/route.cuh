@@ -308,10 +308,16 @@ __device__ __forceinline__ bool groups_exact(const T* __restrict__ row, const Ro
 //   products 2^-24 each.  Sigmoid s = 1 / (1 + e): at most 2^-22 + 2^-23 +
 //   2^-24 of it, and in absolute terms s (1 - s) 2^-22 + s (2^-23 + 2^-24) <=
 //   2^-22.  Softmax: 2^-19 + |l - max| 2^-24 of the score (21 additions for 512
-//   experts), taken for up to 30 below the maximum; beside a bias, in absolute
-//   terms, 2^-22 for the exponential, as much for the sum's, 2^-23 + 2^-23 for
-//   the quotient and the rounded sum and e^-1 2^-24 for the argument, of the
-//   largest score.  The bias' addition: 2^-24 of the choice value.
+//   experts), taken for up to 30 below the maximum.
+//   Softmax beside a bias, in units of 2^-24 of the largest score.  Each value:
+//   e^-a (4 for the exponential + a for its argument, a = max - l, + 1 for the
+//   product) <= 5.  The common divisor: 4 for the exponentials, at most 3.9 for
+//   their arguments (sum of a e^-a over sum of e^-a, 511 experts at the worst a),
+//   1 for the rounded sum, 2 for the reciprocal: 10.9, but it moves two values by
+//   that times their difference.  Two values so come out in order from 2 * 5 +
+//   10.9 = 20.9 units (1.25e-6) apart, where 2 * 7.5e-7 is taken, and two sums of
+//   two from 4 * 5 + 2 * 10.9 (2.5e-6), where twice that is.  The bias' addition
+//   and that of a group's two: 2^-24 of the choice value each, 2^-23 taken.
 __device__ __forceinline__ float rcp_approx(float v) {
     float r;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
