@@ -764,8 +764,8 @@ bnn_status bnn_fp8_pack(const void* x, bnn_dtype dt, int64_t x_rows, int64_t K, 
  *   on it is infinite and C infinite or NaN, whatever the codes are.
  *   M, N >= 0, K >= 1, each below 2^31 - 512.
  *   Errors: INVALID_ARG, ALIGNMENT (A, W not 16-byte aligned, lda / ldw not a
- *   multiple of 16), UNSUPPORTED (a stride of 2^40 bytes, more than 2^30 tiles),
- *   CUDA. */
+ *   multiple of 16), UNSUPPORTED (a stride of 2^40 bytes, more than 2^30 tiles of
+ *   256 x 128 outputs or 2^27 of 128 weight rows), CUDA. */
 bnn_status bnn_fp8_gemm(const uint8_t* A, int64_t lda, const float* a_scales, int64_t ld_as, const uint8_t* W,
                         int64_t ldw, const float* w_scales, int64_t ld_ws, int64_t M, int64_t N, int64_t K, void* out,
                         bnn_dtype out_dt, int64_t ld_out, bnn_stream_t stream);
@@ -817,11 +817,12 @@ typedef struct bnn_route_params {
  *   times scale.
  * Scores and comparisons are in fp64 (a choice is a whole number: fp32 ties
  * would make it depend on rounding), and so are the weights, rounded to fp32
- * once; equal values go to the lowest index.  An
- * expert whose logit is NaN or -inf, or whose bias is NaN or -inf, is never
- * chosen; a logit of +inf counts as the largest finite fp32.  A token with
- * fewer than k experts to choose from gets index -1 and weight 0 in its last
- * slots.
+ * once; equal values go to the lowest index.  (Values whose order hangs on the
+ * last bit of an fp64 exponential, or of a softmax's fp64 sum, may come either
+ * way round.)  An expert whose logit is NaN or -inf, or whose bias is NaN or
+ * -inf, is never chosen; a logit of +inf counts as the largest finite fp32.  A
+ * token with fewer than k experts to choose from gets index -1 and weight 0 in
+ * its last slots.
  *   logits   device [T, ld], ld >= E, dtype dt; E 1 .. 512.
  *   idx      device int32 [T, k], contiguous; weights device fp32 [T, k].
  *   offsets, row_token, slot_row  device int32, all three or none (NULL): the

@@ -565,11 +565,6 @@ _I32 = frozenset((torch.int32,))
 # The calls below are often shorter on the GPU than a Python call is long, so
 # their wrappers read each tensor's attributes once and pass plain integers.
 
-def _current_device() -> int:
-    torch.cuda._lazy_init()
-    return torch._C._cuda_getDevice()
-
-
 def _rows(t: torch.Tensor, dtypes, dev: int):
     """(rows, columns, row stride) of a matrix of one of ``dtypes`` on device ``dev``, elements of a row adjacent; the
     stride of a single row, which torch leaves arbitrary, is at least its width."""
@@ -609,7 +604,7 @@ def bnn_fp8_pack(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, blo
                  row_index: Optional[torch.Tensor] = None, K: Optional[int] = None, stream=None) -> None:
     """x [x_rows, K] (fp32/bf16, unit inner stride) -> e4m3 codes [rows, ld] (float8_e4m3fn or uint8) and block-major
     fp32 scales [ceil(K / 128), row blocks].  row_index int32 [rows]: the row of x of each packed row (block_rows 1)."""
-    dev = _current_device()
+    dev = torch.cuda.current_device()
     x_rows, Kx, ld_x = _rows(x, _REAL, dev)
     rows, cols, ld_c = _rows(codes, _CODES, dev)
     kb, nr, ld_s = _rows(scales, _F32, dev)
@@ -627,7 +622,7 @@ def bnn_fp8_gemm(A: torch.Tensor, a_scales: torch.Tensor, W: torch.Tensor, w_sca
                  out: torch.Tensor, stream=None) -> None:
     """out [M, N] (fp32/bf16) = A W^T for codes A [M, lda], W [N, ldw] with scales [ceil(K / 128), M] (one per row)
     and [ceil(K / 128), ceil(N / 128)] (one per 128 rows)."""
-    dev = _current_device()
+    dev = torch.cuda.current_device()
     M, ka, lda = _rows(A, _CODES, dev)
     N, kw, ldw = _rows(W, _CODES, dev)
     ba, na, lsa = _rows(a_scales, _F32, dev)
@@ -645,7 +640,7 @@ def bnn_fp8_gemm_grouped(A: torch.Tensor, a_scales: torch.Tensor, offsets: torch
                          w_scales: torch.Tensor, K: int, out: torch.Tensor, stream=None) -> None:
     """Rows offsets[e] .. offsets[e + 1] of A [R, lda] times W[e]^T for W [E, N, ldw], w_scales
     [E, ceil(K / 128), ceil(N / 128)], offsets int32 [E + 1] on the device; out [R, N]."""
-    dev = _current_device()
+    dev = torch.cuda.current_device()
     R, ka, lda = _rows(A, _CODES, dev)
     ba, na, lsa = _rows(a_scales, _F32, dev)
     mo, no, ldo = _rows(out, _REAL, dev)
@@ -679,7 +674,7 @@ def bnn_route(logits: torch.Tensor, idx: torch.Tensor, weights: torch.Tensor, sc
               row_token: Optional[torch.Tensor] = None, slot_row: Optional[torch.Tensor] = None, stream=None) -> None:
     """Choose k experts per token: logits [T, E] (fp32/bf16) -> idx int32 [T, k], weights fp32 [T, k]; with offsets
     int32 [E + 1], row_token int32 [T * k] and slot_row int32 [T, k] also the plan of rows by expert."""
-    dev = _current_device()
+    dev = torch.cuda.current_device()
     T, E, ld = _rows(logits, _REAL, dev)
     ti, k = idx.shape
     n = T * k
@@ -699,7 +694,7 @@ def bnn_route(logits: torch.Tensor, idx: torch.Tensor, weights: torch.Tensor, sc
 def bnn_route_combine(Y: torch.Tensor, slot_row: torch.Tensor, weights: torch.Tensor, out: torch.Tensor,
                       stream=None) -> None:
     """out [T, N] = sum over j of weights[t, j] * Y[slot_row[t, j]] (Y [R, N], fp32/bf16)."""
-    dev = _current_device()
+    dev = torch.cuda.current_device()
     R, N, ldy = _rows(Y, _REAL, dev)
     to, no, ldo = _rows(out, _REAL, dev)
     T, k = weights.shape

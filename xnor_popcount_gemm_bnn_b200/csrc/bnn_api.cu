@@ -1911,6 +1911,10 @@ bnn_status launch_fp8_gemm_as(const Fp8Operands& o, const bnn::Fp8Gemm& g, cudaS
     //   64 experts of 4 rows 82 / 85 / 93 / 134, of 16 rows 120 / 93 / 99 / 142;
     //   32 experts of 16 rows 72 / 57 / 50 / 82, of 32 rows 121 / 77 / 62 / 78,
     //   of 64 rows 219 / 126 / 89 / 78.
+    // The average is all the host knows: where few experts get most rows, each
+    // reads its weights again for every 16, 32 or 64 of them on the CTAs of its own
+    // tiles.  64 experts, even / half the rows with one / all with one: 128 rows
+    // 83 / 87 / 74 us, 512 rows 88 / 128 / 160, 2048 rows 99 / 244 / 387.
     // Dense, 128 rows: 11008 x 4096 split 18.7, pair 21; 4096 x 11008 16 and 24.
     if (rows <= (grouped ? 6 : 16)) return launch_fp8_split<16, T>(o, g, stream);
     if (rows <= (grouped ? 14 : 32)) return launch_fp8_split<32, T>(o, g, stream);
@@ -1940,7 +1944,13 @@ bnn_status launch_fp8_pack(const void* x, int64_t x_rows, int64_t K, int64_t ld_
     if (block_rows == 1) {
         // Several blocks per warp share the scale's division (four vectors of
         // four blocks, fp32 two; narrow eight blocks); when that leaves the SMs
-        // without warps, as few as possible.
+        // fewer than 16 warps each, as few as possible.  Measured, us, several /
+        // one, at 0.4, 1 and 4 times the border: rows of 4096 bf16 2.3 / 2.7 at 512,
+        // 3.0 / 4.0 at 1184, 11.1 / 15.3 at 4736; of 4096 fp32 2.1 / 2.1 at 256, 3.9 /
+        // 3.7 at 768, 9.9 / 10.7 at 2368; of 4090 fp32 (narrow) 2.2 / 2.9 at 256, 2.9 /
+        // 4.3 at 512, 10.1 / 17.5 at 2368; 64 rows of any 2.1 to 2.9 / 1.6 to 1.7.  Rows
+        // that end before a warp's several vectors lose a little: 8192 of 1024 bf16
+        // 7.8 / 7.2.
         constexpr int U = wide ? (sizeof(T) == 2 ? 4 : 2) : 8, per = wide ? 512 : bnn::fp8::BLOCK;
         const bool many = rows * ceil_div(K, per * U) >= 16 * (int64_t)sm_count();
         const dim3 grid((unsigned)ceil_div(rows, 8),
@@ -2001,8 +2011,10 @@ bnn_status launch_route_as(const void* logits, const bnn::RouteParams& params, c
     constexpr int VB = NI * (int)sizeof(T) < 16 ? NI * (int)sizeof(T) : 16;
     bnn::RouteParams p = params;
     p.vec = aligned(l, VB) && p.ld * (int64_t)sizeof(T) % VB == 0 && p.E * (int64_t)sizeof(T) % VB == 0 ? 1 : 0;
-    // Few tokens with a plan: both in one CTA (a second launch costs more
-    // than the SMs it leaves idle).
+    // Few tokens with a plan: both in one CTA (a second launch costs more than
+    // the SMs it leaves idle), a token per warp.  One CTA / two launches, us: 4 of
+    // 64 experts 4.0 / 5.3 at 16 tokens, 5.8 / 5.3 at 24; 8 of 256 5.9 / 7.1 at 16,
+    // 8.9 / 7.1 at 24.
     if (plan.offsets != nullptr && p.T <= SMALL_T)
         return launch_clusters(bnn::route_small_kernel<T, NI>, dim3(1), PLAN_THREADS, bnn::route_plan_smem(p.E), 1,
                                stream, l, p, plan.offsets, plan.row_token, plan.slot_row);

@@ -20,7 +20,7 @@ namespace bnn {
 namespace fp8 {
 constexpr int BLOCK = 128;                  // elements of K (and weight rows) per scale
 constexpr float CODE_MAX = 448.0f;
-constexpr float SCALE_MIN = 1.17549435e-38f;   // 2^-126: the reciprocal stays finite
+constexpr float SCALE_MIN = 1.17549435e-38f;   // 2^-126, the least normal number: no scale is subnormal or 0
 
 __device__ __forceinline__ float block_scale(float amax) { return fmaxf(__fdiv_rn(amax, CODE_MAX), SCALE_MIN); }
 
@@ -265,9 +265,10 @@ constexpr int LANES = BLOCK / 16;           // lanes per block of a row
 // Blocks of 1 x 128.  Eight lanes share a block; a warp takes U x 512 elements
 // of one row and reads every element once.  Warps of consecutive rows run next
 // to each other, so their scales, consecutive in memory, meet in L2.  Measured:
-// 16384 rows of 4096 bf16 gathered from 4096, 26.8 us (134 MB read through L2, 69
-// MB written); instruction issue, 61 %, and the latency of two dependent loads
-// bound it.  4096 x 4096 fp32 15 us, 0.86 of the measured HBM rate.
+// 16384 rows of 4096 bf16 gathered from 4096, 27 to 28 us (134 MB read through L2,
+// 69 MB written): a row is read, reduced and divided once for each of its packed
+// rows (61 % of the issue slots, two dependent loads before the first element).
+// 4096 x 4096 fp32 15 us, 0.86 of the measured HBM rate.
 template <typename T, int ALIGN, int U>
 __global__ void __launch_bounds__(256)
 fp8_pack_rows_kernel(const T* __restrict__ x, int64_t x_rows, int64_t K, int64_t ld_x,
@@ -443,12 +444,9 @@ fp8_pack_blocks_kernel(const T* __restrict__ x, int64_t rows, int64_t K, int64_t
 }
 
 // The same for rows of any alignment: a warp takes 16 rows of the block.
-// 11008 x 4090 fp32 (rows on 8-byte boundaries) 44 us, 0.78 of the measured HBM
-// rate; with 16 elements per lane in 8-byte loads it took 46 us before the
-// quotient was refined, this layout 40.
-// 11008 x 4090 fp32 (rows on 8-byte boundaries) 44 us, 0.78 of the measured HBM
-// rate; with 16 elements per lane in 8-byte loads it took 46 us before the
-// quotient was refined, this layout 40.
+// 11008 x 4090 fp32 (rows on 8-byte boundaries) 44 to 47 us, 0.78 to 0.73 of the
+// measured HBM rate; with 16 elements per lane in 8-byte loads it took 46 us
+// before the quotient was refined, this layout 40.
 template <typename T, int V>
 __global__ void __launch_bounds__(256)
 fp8_pack_blocks_narrow_kernel(const T* __restrict__ x, int64_t rows, int64_t K, int64_t ld_x,

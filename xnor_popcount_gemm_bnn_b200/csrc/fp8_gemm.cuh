@@ -303,9 +303,9 @@ __device__ __forceinline__ void add_parts(const Fp8Parts& p, const Fp8Gemm& g, i
 // With S > 1 the CTAs leave their partial sums in shared memory and each adds
 // the columns r, r + S, ... of all of them in rank order: the same sum on every run.
 // Bound by the weights' stream and, when it is short, by the launch: 11008 x 4096
-// and one row 10.5 us (45 MB, 0.66 of the measured HBM rate; 10.0 without the
-// parts' addition), 64 experts of 2048 x 4096 with 128 rows 66 us (387 MB read,
-// 0.89).  The scales, whose loads a register would have waited for in every
+// and one row 10.4 to 11.1 us (45 MB, 0.66 of the measured HBM rate; 0.5 us of it
+// the parts' addition), 64 experts of 2048 x 4096 with 128 rows 65 to 72 us (387 MB
+// read, 0.91 to 0.82).  The scales, whose loads a register would have waited for in every
 // block, were what bound it first (13.8 and 107 us).
 template <int NT, bool DEEP, typename T>
 __global__ void __launch_bounds__(f8s::Cfg<NT, DEEP>::THREADS, f8s::Cfg<NT, DEEP>::PER_SM)
@@ -650,9 +650,11 @@ struct Fp8Tiles {
 // run while the epilogue adds this one.  What bounds the kernel is the
 // latency of each role's loop per block (wait, issue, hand on), which is why
 // the loops hold nothing else and ask for the next block's barriers early.
-// Measured: 8192 x 8192 x 8192 to bf16 480 us = 2.29 PFLOP/s, 0.71 of twice the
-// measured bf16 rate (tensor pipe active 46 %); without the sums over blocks,
-// one accumulation over K, the same loop took 401 us.  On the way: a release
+// Measured: 8192 x 8192 x 8192 to bf16 480 to 490 us in a call by itself = 2.26
+// PFLOP/s, 0.70 of twice the measured bf16 rate (tensor pipe active 46 %), and 550 to
+// 570 us = 1.96 in a loop under the power limit, 0.72 of twice the sustained rate;
+// without the sums over blocks, one accumulation over K, the single call took 401
+// us.  The 256-column variants spill 20 (fp32) and 56 bytes (bf16) a thread.  On the way: a release
 // over the cluster in every hand-back cost 470 us, scales loaded into registers
 // 280, copies and MMAs issued by a lane the compiler did not know to be alone 60.
 // The finished tile is rounded, put into shared memory (16-byte chunks swizzled

@@ -782,7 +782,8 @@ __device__ __forceinline__ float ldg_if(const __nv_bfloat16* p, int on) {
 // token's rows and weights, and the loads of J rows are in flight together
 // (predicated: a branch would wait for each).  V = 16 bytes of T
 // where every row of Y and out allows it, else 1.  4096 tokens of 4 rows of 4096
-// bf16: 29.4 us, 0.87 of the measured HBM rate; odd rows 43 us.
+// bf16: 29.4 us, 0.87 of the measured HBM rate; odd rows, one element per load,
+// 43 us.
 constexpr int kCombineThreads = 256;
 template <typename T, typename O, int V, int C, int J>
 __global__ void __launch_bounds__(kCombineThreads)
