@@ -542,9 +542,10 @@ __device__ __forceinline__ void route_token(const T* __restrict__ row, const Rou
 }
 
 // (Registers limited for occupancy: only route_exact() would take more.)  Bound
-// by instruction latency, about 900 a token and 28 % of the issue slots: 8192
-// tokens, 256 experts 12 us, with groups 14 us (21 us with groups on the
-// border left to route_exact(), whose last token the launch waits for).
+// by issue and latency of about 900 instructions a token: 45 % of the issue slots
+// in a cold launch of 20 us, about 65 % of them in a stream of calls.  8192 tokens,
+// 256 experts 12 us, with groups 14 us (21 us with groups on the border left to
+// route_exact(), whose last token the launch waits for).
 // Everything in fp64 and by shuffles it took 62 us.
 template <typename T, int NI>
 __global__ void __launch_bounds__(256, 4) route_topk_kernel(const T* __restrict__ logits, RouteParams p) {
